@@ -64,7 +64,8 @@ typedef struct tc_layout {
  * {1, 2, 4, 8, 16}).  TC_B128 is a 16-byte struct such as four int32. */
 enum tc_dtype {
   TC_U8 = 0, TC_I8 = 1, TC_F16 = 2, TC_BF16 = 3, TC_F32 = 4, TC_I32 = 5,
-  TC_F64 = 6, TC_I64 = 7, TC_B128 = 8
+  TC_F64 = 6, TC_I64 = 7, TC_B128 = 8,
+  TC_E4M3 = 9   /* 8-bit floats (1-4-3 bits, largest 448, no infinities); a copy moves the byte */
 };
 
 /* Return codes: 0 = success, negative = error (tc_last_error() has the reason). */
@@ -334,6 +335,117 @@ typedef struct tc_permute_info {
 
 int tc_wave_permute_plan(const tc_layout* src_layout, const tc_layout* dst_layout, int dtype,
                          tc_permute_info* out);
+
+/*
+ * ---- Paged key-value cache ---------------------------------------------------------------------
+ *
+ * The caches that attention reads, as layouts: keys and values lie in pools of pages, each a
+ * TileLayout of logical shape (pages, page_size, heads, head_dim) with any page, row and head
+ * strides (rows of all heads together, or a head's rows together: the strides say which), and a
+ * block table names each sequence's pages in order.  Row i of sequence b is row i % page_size of
+ * page block_table[b][i / page_size].
+ *
+ *   dtype         TC_F16 or TC_BF16 (k_scale = v_scale = NULL), or TC_E4M3: each row and head holds
+ *                 8-bit codes and one fp32 scale, the value being code * scale
+ *   k, v          device pointers; the layouts' innermost stride is 1 (where head_dim > 1), pointers
+ *                 and the other byte strides are multiples of 16 (TC_E_ALIGN)
+ *   k_scale, ...  fp32, logical shape (pages, page_size, heads), any strides (TC_E4M3 only)
+ *   head_dim      a multiple of 16, at most 256
+ *
+ * Keys and values have one shape.  Strides are 0 or more.  Tables and lengths are int32 on the device, read by the
+ * kernels: the host calls never wait for them, so a captured graph replays with new contents.  What
+ * they may hold is bounded in the kernels: a page outside [0, pages) is no page (its rows count as
+ * absent), lengths are taken as at least 0 and at most what the table's columns and max_len hold.
+ * Two sequences may share pages that are only read.
+ */
+typedef struct tc_paged_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  tc_layout k_layout, v_layout;
+  tc_layout k_scale_layout, v_scale_layout;
+  int32_t dtype;
+  int32_t reserved;
+} tc_paged_cache;
+
+/*
+ * Copies new tokens' keys and values into the cache.  k_new, v_new: (tokens, heads, head_dim), any
+ * token and head strides (slices of a fused projection's rows), innermost stride 1, of `dtype`
+ * TC_F16 or TC_BF16: the cache's own type, moved as bits, or anything into a TC_E4M3 cache, rounded:
+ *
+ *   scale = max |x| / 448 over the row (1 where that is below the smallest normal fp32),
+ *   code  = x / scale to the nearest even code
+ *
+ * (a row with an infinity or NaN reads back as NaN where scale * code is).  block_table:
+ * (batch, columns).  seq_lens (batch, contiguous) counts the rows after the append.  With
+ * token_starts (batch + 1, contiguous, ascending) tokens starts[b] .. starts[b+1] - 1 are the last
+ * rows of sequence b, in order, and tokens from starts[batch] on are padding; without (NULL), token b
+ * is sequence b's last row (tokens == batch).  Tokens whose row lies outside the table or on no page are
+ * not written, nor is anything else of the pool.  weights (batch, heads, capacity), may be NULL:
+ * set to 0 for the appended rows (see tc_paged_attention).  Rows that two tokens of one call name (pages shared by
+ * sequences that both append to them) hold either token's values.
+ * Errors: TC_E_NULL, TC_E_RANK, TC_E_EXTENT, TC_E_DTYPE, TC_E_ALIGN, TC_E_NONINJECTIVE (cache rows
+ * overlap), TC_E_ALIAS (new rows inside the pools), TC_E_RANGE, TC_E_HIP.
+ */
+int tc_paged_append(const tc_paged_cache* cache, const void* k_new, const tc_layout* k_layout, const void* v_new,
+                    const tc_layout* v_layout, int dtype, const int32_t* block_table,
+                    const tc_layout* table_layout, const int32_t* seq_lens, const int32_t* token_starts,
+                    float* weights, const tc_layout* weights_layout, void* stream);
+
+/*
+ * Attention of one new token a sequence over its cache.  q, out: (batch, q_heads, head_dim) of `dtype`
+ * (TC_F16 or TC_BF16: the cache's type, or either over a TC_E4M3 cache), q_heads = group * heads,
+ * query head h reading cache head h / group.  For the n = seq_lens[b] rows of sequence b (at most
+ * max_len):
+ *
+ *   x_i = scale * q . k_i     lse = log sum_i exp x_i     p_i = exp(x_i - lse)     out = sum_i p_i v_i
+ *
+ * Sums, maxima and products accumulate in fp32, out is rounded once.  No row, or none with x_i above
+ * -infinity: out = 0, lse = -infinity.  Rows past n and rows on no page are never used, whatever
+ * they hold.  lse (batch, q_heads), fp32, may be NULL.  weights_out (batch, heads, capacity >= max_len), fp32, may be NULL:
+ * receives weights[b][h][i] + the sum of p_i over the head's group, for i < n; weights (the same shape)
+ * may be weights_out itself (sums grow in place) or not overlap it; rows from n on are left as they are.
+ * workspace: tc_paged_attention_workspace(...) bytes of device memory, 16-byte aligned, used until
+ * the call's kernels end and by no other call meanwhile; may be NULL where that is 0.
+ * Errors: as above; TC_E_ARG (workspace too small, bad scale or sizes), TC_E_ALIAS (an output overlaps
+ * an input).
+ */
+int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layout* q_layout, void* out,
+                       const tc_layout* out_layout, int dtype, const int32_t* block_table,
+                       const tc_layout* table_layout, const int32_t* seq_lens, int64_t max_len, float scale,
+                       float* lse, const tc_layout* lse_layout, const float* weights,
+                       const tc_layout* weights_layout, float* weights_out, const tc_layout* weights_out_layout,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tc_paged_attention needs for these sizes (0: none), or a negative status.
+ * Host only. */
+int64_t tc_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim,
+                                     int64_t max_len, int with_weights);
+
+/*
+ * Shrinks sequences to `budget` rows a head by their accumulated attention weights.  For each sequence b
+ * and head h with n = seq_lens[b] rows (at most max_len): all rows if n <= budget; else the last
+ * `recent` rows and, of the others, the budget - recent with the greatest weights[b][h][i] (a NaN
+ * counts as greater than any number, equal weights go to the lower row).  The rows kept, in
+ * their order, are copied into rows 0 .. lens_out[b] - 1 of the sequence's pages in `dst`, bits
+ * unchanged, scales with them: dst_table (batch, columns) names them, pages of another pool or pages of
+ * the same pool (dst may equal src) that no row kept lies on.  Every head keeps its own rows.
+ *   weights        (batch, heads, capacity >= max_len), fp32
+ *   lens_out       (batch), contiguous: min(n, budget)
+ *   kept           (batch, heads, columns >= min(budget, max_len)), int32: the rows kept, -1 past lens_out[b]
+ *   weights_out    (batch, heads, capacity >= min(budget, max_len)), fp32, may be NULL: their weights;
+ *                  left as it is past lens_out[b]
+ * A row on no page, on either side, is not copied.  src and dst have the same heads, head_dim and dtype;
+ * their page sizes and strides may differ.  Errors: as above; TC_E_ARG (recent > budget, ...),
+ * TC_E_EXTENT (dst_table holds fewer than min(budget, max_len) rows), TC_E_ALIAS (the pools overlap
+ * without being the same, an output overlaps an input).
+ */
+int tc_paged_evict(const tc_paged_cache* src, const int32_t* block_table, const tc_layout* table_layout,
+                   const int32_t* seq_lens, int64_t max_len, const float* weights, const tc_layout* weights_layout,
+                   const tc_paged_cache* dst, const int32_t* dst_table, const tc_layout* dst_table_layout,
+                   int64_t budget, int64_t recent, int32_t* lens_out, int32_t* kept, const tc_layout* kept_layout,
+                   float* weights_out, const tc_layout* weights_out_layout, void* stream);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int tc_version(void);

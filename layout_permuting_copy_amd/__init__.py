@@ -3,7 +3,8 @@
 Thin ctypes marshalling over the C ABI declared in ``include/tile_copy.h``; every step of
 the copy (planning, kernels) runs in the native library.  Names match the C entry points:
 ``tile_copy``, ``tile_copy_ex``, ``tc_plan``, ``tc_last_error``, ``tc_set_flags``,
-``tc_get_flags``, ``tc_layout_slice``, ``tc_version``.
+``tc_get_flags``, ``tc_layout_slice``, ``tc_version``, ``tc_paged_append``, ``tc_paged_attention``,
+``tc_paged_evict`` (these three take torch tensors and a ``PagedCache``).
 
 Layouts are ``(shape, stride, offset)`` tuples in elements (TileLayout S[shape : stride]),
 or ``TcLayout`` structs.  Source and destination are device pointers (ints) or torch
@@ -22,10 +23,10 @@ LIB_PATH = os.path.join(_PKG, "libtile_copy.so")
 TC_MAX_RANK = 8
 
 # dtypes (enum tc_dtype)
-TC_U8, TC_I8, TC_F16, TC_BF16, TC_F32, TC_I32, TC_F64, TC_I64, TC_B128 = range(9)
-ELEM_BYTES = {TC_U8: 1, TC_I8: 1, TC_F16: 2, TC_BF16: 2, TC_F32: 4, TC_I32: 4, TC_F64: 8, TC_I64: 8, TC_B128: 16}
+TC_U8, TC_I8, TC_F16, TC_BF16, TC_F32, TC_I32, TC_F64, TC_I64, TC_B128, TC_E4M3 = range(10)
+ELEM_BYTES = {TC_E4M3: 1, TC_U8: 1, TC_I8: 1, TC_F16: 2, TC_BF16: 2, TC_F32: 4, TC_I32: 4, TC_F64: 8, TC_I64: 8, TC_B128: 16}
 DTYPE_BY_NAME = {"uint8": TC_U8, "int8": TC_I8, "float16": TC_F16, "bfloat16": TC_BF16, "float32": TC_F32,
-                 "int32": TC_I32, "float64": TC_F64, "int64": TC_I64, "int4vec": TC_B128}
+                 "int32": TC_I32, "float64": TC_F64, "int64": TC_I64, "int4vec": TC_B128, "float8_e4m3fn": TC_E4M3}
 
 # status codes (enum tc_status)
 TC_OK = 0
@@ -156,6 +157,16 @@ def load_library(path: str = LIB_PATH):
     lib.tc_version.restype = ctypes.c_int
     lib.tc_wave_permute_plan.argtypes = [P(TcLayout), P(TcLayout), ctypes.c_int, P(TcPermuteInfo)]
     lib.tc_wave_permute_plan.restype = ctypes.c_int
+    vp, lp, i64, i32 = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    lib.tc_paged_append.argtypes = [vp, vp, lp, vp, lp, i32, vp, lp, vp, vp, vp, lp, vp]
+    lib.tc_paged_append.restype = ctypes.c_int
+    lib.tc_paged_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i32]
+    lib.tc_paged_attention_workspace.restype = ctypes.c_int64
+    lib.tc_paged_attention.argtypes = [vp, vp, lp, vp, lp, i32, vp, lp, vp, i64, ctypes.c_float, vp, lp, vp, lp, vp, lp, vp,
+                                       i64, vp]
+    lib.tc_paged_attention.restype = ctypes.c_int
+    lib.tc_paged_evict.argtypes = [vp, vp, lp, vp, i64, vp, lp, vp, vp, lp, i64, i64, vp, vp, lp, vp, lp, vp]
+    lib.tc_paged_evict.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -332,7 +343,7 @@ def torch_dtype_code(torch_dtype) -> int:
     import torch
     table = {torch.uint8: TC_U8, torch.int8: TC_I8, torch.float16: TC_F16, torch.bfloat16: TC_BF16,
              torch.float32: TC_F32, torch.int32: TC_I32, torch.float64: TC_F64, torch.int64: TC_I64,
-             torch.int16: TC_F16, torch.uint16: TC_F16 if hasattr(torch, "uint16") else TC_F16}
+             torch.float8_e4m3fn: TC_E4M3, torch.int16: TC_F16, torch.uint16: TC_F16 if hasattr(torch, "uint16") else TC_F16}
     return table[torch_dtype]
 
 
@@ -348,3 +359,237 @@ def copy_tensor(dst, src, stream=None) -> dict:
     shape = tuple(int(e) for e in src.shape)
     return tile_copy_ex(src, (shape, tuple(int(s) for s in src.stride()), 0), dst,
                         (shape, tuple(int(s) for s in dst.stride()), 0), code, stream)
+
+
+# ---- paged key-value cache -------------------------------------------------------------------
+
+class TcPagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_layout", TcLayout), ("v_layout", TcLayout),
+                ("k_scale_layout", TcLayout), ("v_scale_layout", TcLayout), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class PagedCache:
+    """A pool of pages of keys and values: torch tensors of logical shape (pages, page_size, heads,
+    head_dim), any strides with an innermost 1 (transpose a head-major pool into this order), float16,
+    bfloat16, or float8_e4m3fn with float32 ``k_scale`` and ``v_scale`` of shape (pages, page_size, heads).
+    Holds the tensors; the layouts are read from them once."""
+
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_c", "_ref", "device")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        if k.dtype != v.dtype:
+            raise ValueError(f"keys are {k.dtype}, values {v.dtype}")
+        self.device = k.device
+        c = TcPagedCache()
+        c.dtype = _paged_dtype(k)
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.k_layout, c.v_layout = make_layout(k.shape, k.stride()), make_layout(v.shape, v.stride())
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (x is not None) != (c.dtype == TC_E4M3):
+                raise ValueError("8-bit caches have k_scale and v_scale, others have none")
+            if x is not None:
+                _want(name, x, "float32")
+                setattr(c, name, x.data_ptr())
+                setattr(c, name + "_layout", make_layout(x.shape, x.stride()))
+        _device_of(self, v, k_scale, v_scale)
+        self._c = c
+        self._ref = ctypes.addressof(c)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    pages = property(lambda self: self._k.shape[0])
+    page_size = property(lambda self: self._k.shape[1])
+    heads = property(lambda self: self._k.shape[2])
+    head_dim = property(lambda self: self._k.shape[3])
+
+
+def _paged_dtype(x) -> int:
+    name = str(x.dtype)[6:]
+    if name not in ("float16", "bfloat16", "float8_e4m3fn"):
+        raise ValueError(f"expected float16, bfloat16 or (a cache) float8_e4m3fn, got {x.dtype}")
+    return DTYPE_BY_NAME[name]
+
+
+def _want(name: str, x, dtype: str) -> None:
+    if str(x.dtype)[6:] != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+
+
+def _device_of(cache, *tensors):
+    dev = cache.device
+    for x in tensors:
+        if x is not None and x.device != dev:
+            raise ValueError(f"tensors on {dev} and {x.device}")
+    return dev
+
+
+def _vector(name: str, x, n: int) -> int:
+    _want(name, x, "int32")
+    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return x.data_ptr()
+
+
+_layout_cache = {}
+
+
+def _lay(x):
+    """(address, owner) of the TcLayout of a tensor's shape and strides (made once per shape and strides)."""
+    key = (x.shape, x.stride())
+    at = _layout_cache.get(key)
+    if at is None:
+        if len(_layout_cache) >= 4096:
+            _layout_cache.clear()
+        lay = make_layout(key[0], key[1])
+        at = _layout_cache[key] = (ctypes.addressof(lay), lay)
+    return at
+
+
+class _Launch:
+    """The tensors' device made current, and the stream the call goes to."""
+
+    __slots__ = ("dev", "prev", "stream", "handle")
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.prev = dev, stream, None
+
+    def __enter__(self):
+        import torch
+        if self.dev.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, not {self.dev}")
+        if torch.cuda.current_device() != self.dev.index:
+            self.prev = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        self.handle = torch.cuda.current_stream().cuda_stream if self.stream is None else _stream(self.stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            import torch
+            torch.cuda.set_device(self.prev)
+
+    def empty(self, n: int, dtype, shape=None):
+        """Memory for this call, allocated on its stream: another stream's next use waits its turn."""
+        import torch
+        if self.stream is None or self.handle == torch.cuda.current_stream().cuda_stream:
+            return torch.empty(shape or n, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=self.dev)):
+            return torch.empty(shape or n, dtype=dtype, device=self.dev)
+
+
+def tc_paged_append(cache: PagedCache, k, v, block_table, seq_lens, token_starts=None, weights=None,
+                    stream=None) -> None:
+    """Copies new tokens' keys and values, (tokens, heads, head_dim) float16 or bfloat16 with any outer
+    strides, into the cache: as they are, or rounded to e4m3 with a scale a row and head.
+
+    ``block_table`` (batch, columns) int32 names each sequence's pages, ``seq_lens`` (batch) int32 counts its
+    rows after the append.  Token b becomes the last row of sequence b; with ``token_starts`` (batch + 1) int32,
+    tokens starts[b] .. starts[b + 1] - 1 become its last rows and tokens past starts[batch] are padding.
+    ``weights`` (batch, heads, capacity) float32, if given, is zeroed for the new rows."""
+    lib = load_library()
+    dev = _device_of(cache, k, v, block_table, seq_lens, token_starts, weights)
+    if k.dtype != v.dtype:
+        raise ValueError(f"keys are {k.dtype}, values {v.dtype}")
+    _want("block_table", block_table, "int32")
+    batch = block_table.shape[0]
+    lens = _vector("seq_lens", seq_lens, batch)
+    starts = None if token_starts is None else _vector("token_starts", token_starts, batch + 1)
+    if weights is not None:
+        _want("weights", weights, "float32")
+    kl, vl, tl = _lay(k), _lay(v), _lay(block_table)
+    wl = (None, None) if weights is None else _lay(weights)
+    with _Launch(dev, stream) as at:
+        _check(lib.tc_paged_append(cache._ref, k.data_ptr(), kl[0], v.data_ptr(), vl[0], _paged_dtype(k),
+                                   block_table.data_ptr(), tl[0], lens, starts,
+                                   None if weights is None else weights.data_ptr(), wl[0], at.handle))
+
+
+def tc_paged_attention(q, cache: PagedCache, block_table, seq_lens, scale: Optional[float] = None,
+                       max_len: Optional[int] = None, out=None, lse=None, weights=None, weights_out=None,
+                       stream=None):
+    """Attention of one new token a sequence, ``q`` (batch, q_heads, head_dim), over its cached rows; returns ``out``.
+
+    ``scale`` defaults to head_dim ** -0.5.  ``max_len`` bounds ``seq_lens`` (default: what the table's columns
+    hold); a tight bound saves launches and memory.  ``lse`` (batch, q_heads) float32 receives the log of the
+    sums.  ``weights`` (batch, heads, capacity) float32: ``weights_out`` (default: ``weights`` itself) receives
+    weights plus each row's attention weight summed over the query heads of its cache head."""
+    import torch
+    lib = load_library()
+    dev = _device_of(cache, q, block_table, seq_lens, out, lse, weights, weights_out)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be (batch, q_heads, head_dim), block_table (batch, columns)")
+    _want("block_table", block_table, "int32")
+    batch, q_heads, dim = q.shape
+    lens = _vector("seq_lens", seq_lens, batch)
+    if max_len is None:
+        max_len = block_table.shape[1] * cache.page_size
+    if scale is None:
+        scale = dim ** -0.5
+    if weights_out is None:
+        weights_out = weights
+    elif weights is None:
+        raise ValueError("weights_out without weights")
+    for name, x in (("lse", lse), ("weights", weights), ("weights_out", weights_out)):
+        if x is not None:
+            _want(name, x, "float32")
+    ql, tl = _lay(q), _lay(block_table)
+    none = (None, None)
+    ll = none if lse is None else _lay(lse)
+    wl, wol = (none, none) if weights is None else (_lay(weights), _lay(weights_out))
+    with _Launch(dev, stream) as at:
+        if out is None:
+            out = at.empty(0, q.dtype, q.shape)
+        elif out.dtype != q.dtype:
+            raise ValueError(f"out is {out.dtype}, q {q.dtype}")
+        ol = _lay(out)
+        need = lib.tc_paged_attention_workspace(batch, q_heads, cache.heads, dim, max_len, weights is not None)
+        if need < 0:
+            _check(int(need))
+        work = at.empty(need, torch.uint8) if need else None
+        _check(lib.tc_paged_attention(
+            cache._ref, q.data_ptr(), ql[0], out.data_ptr(), ol[0], _paged_dtype(q), block_table.data_ptr(), tl[0], lens,
+            max_len, scale, None if lse is None else lse.data_ptr(), ll[0],
+            None if weights is None else weights.data_ptr(), wl[0],
+            None if weights_out is None else weights_out.data_ptr(), wol[0],
+            None if work is None else work.data_ptr(), need, at.handle))
+    return out
+
+
+def tc_paged_evict(src: PagedCache, block_table, seq_lens, weights, dst: PagedCache, dst_table, budget: int,
+                   recent: int = 0, max_len: Optional[int] = None, lens_out=None, weights_out=None, kept=None,
+                   stream=None):
+    """Shrinks every sequence to ``budget`` rows a head: the last ``recent`` and the heaviest others by
+    ``weights`` (batch, heads, capacity) float32, in their order, copied into the pages that ``dst_table`` names
+    in ``dst`` (another pool, or pages of the same one that hold none of the kept rows).  Returns
+    ``(lens_out, kept)``: the new lengths, and the rows kept, (batch, heads, min(budget, max_len)) int32 with -1
+    past the new length.  ``weights_out`` receives the kept rows' weights."""
+    import torch
+    lib = load_library()
+    dev = _device_of(src, block_table, seq_lens, weights, dst, dst_table, lens_out, weights_out, kept)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be (batch, columns)")
+    batch = block_table.shape[0]
+    for name, x, dtype in (("block_table", block_table, "int32"), ("dst_table", dst_table, "int32"),
+                           ("weights", weights, "float32"), ("kept", kept, "int32"), ("weights_out", weights_out, "float32")):
+        if x is not None:
+            _want(name, x, dtype)
+    lens = _vector("seq_lens", seq_lens, batch)
+    held = block_table.shape[1] * src.page_size
+    max_len = held if max_len is None else min(max_len, held)
+    with _Launch(dev, stream) as at:
+        if lens_out is None:
+            lens_out = at.empty(batch, torch.int32)
+        if kept is None:
+            kept = at.empty(0, torch.int32, (batch, src.heads, max(0, min(budget, max_len))))
+        tl, wl, dl, kl = _lay(block_table), _lay(weights), _lay(dst_table), _lay(kept)
+        wol = (None, None) if weights_out is None else _lay(weights_out)
+        _check(lib.tc_paged_evict(src._ref, block_table.data_ptr(), tl[0], lens, max_len, weights.data_ptr(), wl[0],
+                                  dst._ref, dst_table.data_ptr(), dl[0], budget, recent,
+                                  _vector("lens_out", lens_out, batch), kept.data_ptr(), kl[0],
+                                  None if weights_out is None else weights_out.data_ptr(), wol[0], at.handle))
+    return lens_out, kept

@@ -26,7 +26,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "inclu
 RESOURCES = os.path.join(BUILD, "kernel_resources.json")
 REMARK = ["-Rpass-analysis=kernel-resource-usage"]
 SOURCES = ["layout.cpp", "bank.cpp", "plan.cpp", "permute.cpp", "abi.cpp", "kernels.hip", "transpose_eb1.hip", "transpose_eb2.hip",
-           "transpose_eb4.hip", "transpose_eb8.hip", "transpose_eb16.hip"]
+           "transpose_eb4.hip", "transpose_eb8.hip", "transpose_eb16.hip", "paged_abi.cpp", "paged_append.hip",
+           "paged_attention.hip", "paged_evict.hip"]
 
 
 def _run(cmd):

@@ -36,7 +36,7 @@ namespace tc {
 
 int elem_bytes_of(int dtype) {
   switch (dtype) {
-    case TC_U8: case TC_I8: return 1;
+    case TC_U8: case TC_I8: case TC_E4M3: return 1;
     case TC_F16: case TC_BF16: return 2;
     case TC_F32: case TC_I32: return 4;
     case TC_F64: case TC_I64: return 8;
