@@ -62,12 +62,15 @@ struct AttentionArgs {
   const float* weights;
   float* weights_out;  // or NULL
   PagedRows w, wo;
-  float* part_o;    // [batch * q_heads][splits][head_dim]: a split's sum of p v, relative to its maximum
-  float* part_ml;   // [batch * q_heads][splits][2]: its maximum (base 2) and sum
+  float* part_o;    // [workgroups][2][tile_heads][head_dim]: a part's sum of p v, relative to its maximum
+  float* part_ml;   // [workgroups][2][tile_heads][2]: its maximum (base 2) and sum
+  float* final_ml;  // [batch * q_heads][2]: the same of whole rows, where weights are wanted
   float* logits;    // [batch * q_heads][logit_row]: scale * q . k * log2 e, where weights are wanted
   int64_t logit_row;
   int32_t heads, group, head_dim;
-  int32_t max_len, split, splits;
+  int32_t max_len, workgroups, least_units, tile_heads, head_tiles;
+  Div32 unit;       // by the rows of a unit
+  Div32 tiles_div;  // by head_tiles
   float scale_log2e;
 };
 
@@ -86,11 +89,14 @@ struct EvictArgs {
   int32_t max_len, budget, recent;
 };
 
-// How an attention call is split over the cache's length: rows a split, and splits.
-struct PagedSplit {
-  int32_t rows, splits;
+// How an attention call is cut over the cache's length: units of `unit_rows` rows (at most `units` in all), runs
+// of at least least_units of them for up to `workgroups` workgroups, query heads in tiles of tile_heads; whether a
+// sequence's rows can fall to more than one workgroup.
+struct PagedCut {
+  int64_t unit_rows, units, least_units, workgroups, tile_heads, head_tiles;
+  bool cuts;
 };
-PagedSplit paged_split(int64_t batch, int64_t heads, int64_t group, int64_t max_len);
+PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 // Columns a row of the logits workspace holds: max_len rounded up to whole tiles.
 int64_t paged_logit_row(int64_t max_len);
 

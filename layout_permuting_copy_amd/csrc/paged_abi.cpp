@@ -267,19 +267,24 @@ void attention_sizes(int64_t batch, int64_t q_heads, int64_t heads, int64_t head
 
 // Floats of each part of the workspace.
 struct Workspace {
-  tc::PagedSplit split;
-  int64_t o, ml, logits;
-  int64_t bytes() const { return 4 * (o + ml + logits); }
+  tc::PagedCut cut;
+  int64_t o, ml, final_ml, logits;
+  int64_t bytes() const { return 4 * (o + ml + final_ml + logits); }
 };
 Workspace workspace_of(int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_len, bool weights) {
   Workspace w{};
   if (batch == 0 || q_heads == 0) return w;
-  w.split = tc::paged_split(batch, heads, q_heads / heads, max_len);
-  const int64_t rows = batch * q_heads, splits = w.split.splits;
-  need(__int128(rows) * splits * head_dim < kLim && __int128(rows) * max_len < kLim, TC_E_RANGE, "workspace beyond 2^58");
-  if (splits > 1) w.o = rows * splits * head_dim;
-  if (splits > 1 || weights) w.ml = (rows * splits * 2 + 3) / 4 * 4;
-  if (weights) w.logits = rows * tc::paged_logit_row(max_len);
+  w.cut = tc::paged_cut(batch, heads, q_heads / heads, head_dim, max_len);
+  need(w.cut.units < (int64_t(1) << 31) && __int128(batch) * q_heads * max_len < kLim, TC_E_RANGE,
+       "batch, heads and max_len beyond what the kernels count");
+  if (w.cut.cuts) {
+    w.o = w.cut.workgroups * 2 * w.cut.tile_heads * head_dim;
+    w.ml = w.cut.workgroups * 2 * w.cut.tile_heads * 2;
+  }
+  if (weights) {
+    w.final_ml = (batch * q_heads * 2 + 3) / 4 * 4;
+    w.logits = batch * q_heads * tc::paged_logit_row(max_len);
+  }
   return w;
 }
 
@@ -403,7 +408,6 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
         if (x != y) apart("two outputs", *x, *y);
     }
     a.pool = c.p;
-    if (c.empty) a.pool.pages = 0;
     a.q = qo.p;
     a.out = oo.p;
     a.qb = qo.s[0], a.qh = qo.s[1], a.ob = oo.s[0], a.oh = oo.s[1];
@@ -413,18 +417,23 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     a.weights = with_weights ? reinterpret_cast<const float*>(w.p) : nullptr;
     a.weights_out = with_weights ? reinterpret_cast<float*>(wo.p) : nullptr;
     float* f = static_cast<float*>(workspace);
-    a.part_o = f;
+    a.part_o = ws.cut.cuts ? f : nullptr;
     a.part_ml = f + ws.o;
-    a.logits = f + ws.o + ws.ml;
+    a.final_ml = with_weights ? f + ws.o + ws.ml : nullptr;
+    a.logits = with_weights ? f + ws.o + ws.ml + ws.final_ml : nullptr;
     a.logit_row = tc::paged_logit_row(max_len);
     a.heads = int32_t(c.heads);
     a.group = int32_t(q_heads / c.heads);
     a.head_dim = int32_t(c.dim);
-    // no row past the table's columns
-    const int64_t held = t.empty ? 0 : std::min<int64_t>(max_len, int64_t(a.table.cols) * c.page_size);
+    // no row past the table's columns, and none of an empty pool
+    const int64_t held = t.empty || c.empty ? 0 : std::min<int64_t>(max_len, int64_t(a.table.cols) * c.page_size);
     a.max_len = int32_t(held);
-    a.split = ws.split.rows;
-    a.splits = ws.split.splits;
+    a.workgroups = int32_t(ws.cut.workgroups);
+    a.least_units = int32_t(ws.cut.least_units);
+    a.tile_heads = int32_t(ws.cut.tile_heads);
+    a.head_tiles = int32_t(ws.cut.head_tiles);
+    a.unit = tc::make_div32(uint32_t(ws.cut.unit_rows));
+    a.tiles_div = tc::make_div32(uint32_t(ws.cut.head_tiles));
     a.scale_log2e = scale * 1.4426950408889634f;
     return launched(tc::launch_paged_attention(a, dtype, c.dtype, stream));
   });
