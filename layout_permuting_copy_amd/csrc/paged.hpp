@@ -50,6 +50,12 @@ struct AppendArgs {
   int32_t heads, head_dim;
 };
 
+// The parts of a sequence that several runs share: `count` of them (0: nothing is shared), the first in slot
+// `slot` of the workgroups of run `run`, the others in slots 0 of the next runs'.
+struct PagedParts {
+  int32_t b, run, count, slot;
+};
+
 struct AttentionArgs {
   PagedPool pool;
   PagedTable table;
@@ -64,13 +70,16 @@ struct AttentionArgs {
   PagedRows w, wo;
   float* part_o;    // [workgroups][2][tile_heads][head_dim]: a part's sum of p v, relative to its maximum
   float* part_ml;   // [workgroups][2][tile_heads][2]: its maximum (base 2) and sum
+  PagedParts* parts;  // by sequence, or by run where there are fewer of those; NULL where nothing can be cut
   float* final_ml;  // [batch * q_heads][2]: the same of whole rows, where weights are wanted
   float* logits;    // [batch * q_heads][logit_row]: scale * q . k * log2 e, where weights are wanted
   int64_t logit_row;
   int32_t heads, group, head_dim;
-  int32_t max_len, workgroups, least_units, tile_heads, head_tiles;
+  int32_t max_len, workgroups, runs, least_units, tile_heads, head_tiles, parts_of_sequences;
+  int64_t units;    // at most
   Div32 unit;       // by the rows of a unit
-  Div32 tiles_div;  // by head_tiles
+  Div32 pairs_div;  // by heads * head_tiles
+  Div32 heads_div;  // by heads
   float scale_log2e;
 };
 
@@ -89,11 +98,11 @@ struct EvictArgs {
   int32_t max_len, budget, recent;
 };
 
-// How an attention call is cut over the cache's length: units of `unit_rows` rows (at most `units` in all), runs
-// of at least least_units of them for up to `workgroups` workgroups, query heads in tiles of tile_heads; whether a
-// sequence's rows can fall to more than one workgroup.
+// How an attention call is cut over the cache's length: units of `unit_rows` rows (at most `units` in all), `runs` runs
+// of at least least_units of them, query heads in tiles of tile_heads, at most `workgroups` workgroups; whether a
+// sequence's rows can fall to more than one run.
 struct PagedCut {
-  int64_t unit_rows, units, least_units, workgroups, tile_heads, head_tiles;
+  int64_t unit_rows, units, least_units, runs, workgroups, tile_heads, head_tiles;
   bool cuts;
 };
 PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);

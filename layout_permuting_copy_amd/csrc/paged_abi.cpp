@@ -261,25 +261,26 @@ void attention_sizes(int64_t batch, int64_t q_heads, int64_t heads, int64_t head
   need(head_dim >= 16 && head_dim <= tc::kPagedMaxHeadDim && head_dim % 16 == 0, TC_E_EXTENT,
        "head_dim must be a multiple of 16 from 16 to 256");
   need(max_len >= 0 && max_len <= (int64_t(1) << 30), TC_E_RANGE, "max_len beyond 2^30");
-  need(batch <= INT32_MAX && q_heads <= INT32_MAX && batch * q_heads <= (int64_t(1) << 30), TC_E_RANGE,
-       "batch * q_heads beyond 2^30");
+  need(batch <= INT32_MAX && q_heads <= 65535 && batch * q_heads <= (int64_t(1) << 30), TC_E_RANGE,
+       "q_heads beyond 65535 or batch * q_heads beyond 2^30");
 }
 
 // Floats of each part of the workspace.
 struct Workspace {
   tc::PagedCut cut;
-  int64_t o, ml, final_ml, logits;
-  int64_t bytes() const { return 4 * (o + ml + final_ml + logits); }
+  int64_t o, ml, parts, final_ml, logits;
+  int64_t bytes() const { return 4 * (o + ml + parts + final_ml + logits); }
 };
 Workspace workspace_of(int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_len, bool weights) {
   Workspace w{};
   if (batch == 0 || q_heads == 0) return w;
   w.cut = tc::paged_cut(batch, heads, q_heads / heads, head_dim, max_len);
-  need(w.cut.units < (int64_t(1) << 31) && __int128(batch) * q_heads * max_len < kLim, TC_E_RANGE,
+  need(w.cut.units < (int64_t(1) << 31) && w.cut.workgroups < (int64_t(1) << 31) && __int128(batch) * q_heads * max_len < kLim, TC_E_RANGE,
        "batch, heads and max_len beyond what the kernels count");
   if (w.cut.cuts) {
     w.o = w.cut.workgroups * 2 * w.cut.tile_heads * head_dim;
     w.ml = w.cut.workgroups * 2 * w.cut.tile_heads * 2;
+    w.parts = w.cut.runs * int64_t(sizeof(tc::PagedParts) / 4);
   }
   if (weights) {
     w.final_ml = (batch * q_heads * 2 + 3) / 4 * 4;
@@ -417,10 +418,12 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     a.weights = with_weights ? reinterpret_cast<const float*>(w.p) : nullptr;
     a.weights_out = with_weights ? reinterpret_cast<float*>(wo.p) : nullptr;
     float* f = static_cast<float*>(workspace);
-    a.part_o = ws.cut.cuts ? f : nullptr;
+    a.part_o = f;
     a.part_ml = f + ws.o;
-    a.final_ml = with_weights ? f + ws.o + ws.ml : nullptr;
-    a.logits = with_weights ? f + ws.o + ws.ml + ws.final_ml : nullptr;
+    a.parts = ws.cut.cuts ? reinterpret_cast<tc::PagedParts*>(f + ws.o + ws.ml) : nullptr;
+    f += ws.o + ws.ml + ws.parts;
+    a.final_ml = with_weights ? f : nullptr;
+    a.logits = with_weights ? f + ws.final_ml : nullptr;
     a.logit_row = tc::paged_logit_row(max_len);
     a.heads = int32_t(c.heads);
     a.group = int32_t(q_heads / c.heads);
@@ -428,12 +431,11 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     // no row past the table's columns, and none of an empty pool
     const int64_t held = t.empty || c.empty ? 0 : std::min<int64_t>(max_len, int64_t(a.table.cols) * c.page_size);
     a.max_len = int32_t(held);
-    a.workgroups = int32_t(ws.cut.workgroups);
+    a.units = ws.cut.units;
     a.least_units = int32_t(ws.cut.least_units);
     a.tile_heads = int32_t(ws.cut.tile_heads);
     a.head_tiles = int32_t(ws.cut.head_tiles);
     a.unit = tc::make_div32(uint32_t(ws.cut.unit_rows));
-    a.tiles_div = tc::make_div32(uint32_t(ws.cut.head_tiles));
     a.scale_log2e = scale * 1.4426950408889634f;
     return launched(tc::launch_paged_attention(a, dtype, c.dtype, stream));
   });

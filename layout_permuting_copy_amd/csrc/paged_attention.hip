@@ -17,22 +17,28 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = 4;
 constexpr int kTile = 32;                       // cache rows a wave takes at a time
 constexpr int kStep = kTile * kAttnWaves;       // and a workgroup
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 constexpr int kCus = 256;
 constexpr float kInf = __builtin_inff();
 
-// Cache bytes: an address whose kind the compiler need not find out.
-typedef const __attribute__((address_space(1))) unsigned char* global_bytes;
+// N bytes of a buffer resource at a lane's offset, `more` bytes on: zeros past its range, which takes the place of a condition
+// on the load (every wait then is for a fixed number of younger loads).  STREAM: read past the caches.
 template <int N, bool STREAM>
-__device__ __forceinline__ void load_cache(global_bytes p, uint32_t* w) {
-  typedef typename Bytes<N>::T T;
-  typedef const __attribute__((address_space(1))) T* P;
-  const T v = STREAM ? __builtin_nontemporal_load((P)p) : *(P)p;
-  if constexpr (N == 4)
-    w[0] = v;
-  else
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) w[i] = v[i];
+__device__ __forceinline__ void load_buffer(Rsrc rsrc, uint32_t off, int more, uint32_t* w) {
+  constexpr int policy = STREAM ? kPolNT : 0;
+  if constexpr (N == 16) {
+    const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, int(off), more, policy));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 8) {
+    const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, int(off), more, policy));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, int(off), more, policy);
+  }
+}
+constexpr uint32_t kBeyond = 0x80000000u;  // an offset past every range (ranges end below 2^31)
+__device__ __forceinline__ Rsrc rows_rsrc(const unsigned char* base, bool live) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(base), 0, live ? int(kBeyond - 1) : 0, kRsrcWord3);
 }
 
 // D = A B + C on 16 x 16 tiles with a contraction of 32.  Lane l (r = l % 16, g = l / 16) holds row r
@@ -85,13 +91,46 @@ __device__ __forceinline__ float finite(float top) {
   return __builtin_amdgcn_fmed3f(top, -3.4028234664e38f, 3.4028234664e38f);
 }
 
-// How the call's work is cut: a sequence of n rows has max(1, ceil(n / unit_rows)) units for each of
-// its `pairs` (cache heads times tiles of query heads); all units in a row, sequence after sequence and
-// pair after pair, are dealt to the workgroups in equal runs (the first `rest` of them one longer).
-// A pair that lies in one run is finished by its workgroup; one that is cut leaves partial results, in
-// slot 0 of a workgroup whose run starts with it and slot 1 of one whose run ends in it.
+// x of this lane's pair and of the lane 16 (D = 16) or 32 away, in either order: a register swapped with a copy of
+// itself by rows or halves.  The copy has to be a register of its own.
+template <int D>
+__device__ __forceinline__ void partners(float x, float* p, float* q) {
+  uint32_t a = __builtin_bit_cast(uint32_t, x), b = a;
+  asm("" : "+v"(b));
+  if constexpr (D == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0], b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0], b = r[1];
+  }
+  *p = __builtin_bit_cast(float, a);
+  *q = __builtin_bit_cast(float, b);
+}
+// The maximum or sum over the four lanes that differ in bits 4 and 5 (the groups g).
+__device__ __forceinline__ float max_of_groups(float x) {
+  float p, q;
+  partners<16>(x, &p, &q);
+  x = __builtin_fmaxf(p, q);
+  partners<32>(x, &p, &q);
+  return __builtin_fmaxf(p, q);
+}
+__device__ __forceinline__ float sum_of_groups(float x) {
+  float p, q;
+  partners<16>(x, &p, &q);
+  x = p + q;
+  partners<32>(x, &p, &q);
+  return p + q;
+}
+
+// How the call's work is cut: a sequence of n rows has max(1, ceil(n / unit_rows)) units; the units of all
+// sequences, one after another, are dealt in equal runs (the first `rest` of them one longer), and a run goes to as
+// many workgroups as there are pairs (a cache head and a tile of its query heads), next to each other in the grid: the
+// heads of one row are read at about the same time.  A sequence within one run is finished there; one that is
+// cut leaves partial results, in slot 0 of the workgroups whose run starts with it and slot 1 of those
+// whose run ends in it.
 struct Cut {
-  uint32_t wgs, each, rest;  // workgroups that get units
+  uint32_t runs, each, rest;
   __device__ __forceinline__ uint32_t start(uint32_t i) const { return i * each + (i < rest ? i : rest); }
   __device__ __forceinline__ uint32_t owner(uint32_t x) const {
     const uint32_t longer = rest * (each + 1);
@@ -100,7 +139,7 @@ struct Cut {
 };
 
 struct Walk {
-  uint32_t total;   // units of all sequences, for one pair
+  uint32_t total;   // units of all sequences
   uint32_t before;  // of the lane's sequences' predecessors
   int per;          // sequences a lane sums: lane * per .. lane * per + per - 1
 };
@@ -133,10 +172,10 @@ __device__ __forceinline__ Walk walk_lengths(const AttentionArgs& a) {
 
 __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t least_each) {
   Cut c;
-  c.wgs = (units + least_each - 1) / least_each;
-  c.wgs = c.wgs < most ? c.wgs : most;
-  c.each = units / c.wgs;
-  c.rest = units - c.each * c.wgs;
+  c.runs = (units + least_each - 1) / least_each;
+  c.runs = c.runs < most ? c.runs : most;
+  c.each = units / c.runs;
+  c.rest = units - c.each * c.runs;
   return c;
 }
 
@@ -161,15 +200,17 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 // The next tile's keys are requested once this tile's logits are formed, its values once this tile's are
 // used, the pages of the one after next before both, so a wave always has loads in flight.  No load of the
 // cache is conditional: rows past the end and rows on no page are read from wherever their index leads inside
-// the pool (page 0 for no page), and what comes back is masked, in the tiles that have such rows.
+// the pool (page 0 for no page), and what comes back is masked, in the tiles that have such rows.  The loop
+// holds the only copy of its code (its first turn requests and computes nothing, its last computes and
+// requests nothing): a short call's time goes into fetching instructions.
 //
-// DP: head_dim rounded up to 64, 128 or 256.  FULL: head_dim is DP; else the key elements past it
-// are cleared (those of Q are, but 0 times infinity is not 0) and the output elements past it not
-// stored.  PAGE16: pages of a multiple of 16 rows, so that a 16-row half lies on one page and its address
-// is scalar; otherwise each lane finds its rows.
+// DP: head_dim rounded up to 64, 128 or 256.  FULL: head_dim is DP; else the key elements past it are
+// zeros (those of Q are, but 0 times infinity is not 0) and the output elements past it not stored.
+// PAGE, the rows known to lie on one page: 16 (a half: its address is scalar, its loads go through a
+// buffer resource), 4 (a lane's value rows of a half) or 1.
 //
 // Bound: HBM (a cache row is read once for all heads of its group).
-template <bool BF16, bool E4M3, int DP, int HT, bool PAGE16, bool FULL>
+template <bool BF16, bool E4M3, int DP, int HT, int PAGE, bool FULL>
 struct Attend {
   static constexpr bool VBF = BF16 || E4M3;       // type of the second product
   static constexpr int EB = E4M3 ? 1 : 2;
@@ -210,10 +251,9 @@ struct Attend {
   int64_t kp, kr, vp, vr, ksp, ksr, vsp, vsr, sc;
   int pool_pages;
   Div32 div;
-  int key_bytes;  // of a row
-  // the lane's byte offsets.  PAGE16: in the 16 rows of a half, of key row r and value row 4 g; otherwise in a row.
-  // Both include the lane's chunk (of a value row past head_dim: the row's first)
-  uint32_t kchunk, krow, vrow, vrow2;
+  // the lane's byte offsets.  PAGE 16: in the 16 rows of a half, of key row r and value row 4 g; otherwise in a row.
+  // Both include the lane's chunk; of a row's chunk past head_dim: beyond the range, or the row's first
+  uint32_t kchunk[FULL ? 1 : KC], vchunk, vchunk2;
 
   __device__ __forceinline__ void pools(const AttentionArgs& a, int b, int h) {
     const PagedPool& p = a.pool;
@@ -232,16 +272,13 @@ struct Attend {
     sc = a.table.sc;
     pool_pages = p.pages;
     div = p.div;
-    key_bytes = a.head_dim * EB;
-    const int e0 = v_element(r, 0), e1 = e0 + DP / 2;
-    kchunk = uint32_t(16 * g);
-    vrow = FULL || e0 < a.head_dim ? uint32_t(e0 * EB) : 0u;
-    vrow2 = FULL || e1 < a.head_dim ? uint32_t(e1 * EB) : 0u;
-    if constexpr (PAGE16) {
-      krow = uint32_t(r) * uint32_t(kr) + kchunk;
-      vrow += uint32_t(4 * g) * uint32_t(vr);
-      vrow2 += uint32_t(4 * g) * uint32_t(vr);
-    }
+    const int bytes = a.head_dim * EB, e0 = v_element(r, 0) * EB, e1 = e0 + DP / 2 * EB;
+    const uint32_t krow = PAGE == 16 ? uint32_t(r) * uint32_t(kr) : 0u, vrow = PAGE == 16 ? uint32_t(4 * g) * uint32_t(vr) : 0u;
+    const uint32_t none = PAGE == 16 ? kBeyond : 0u;
+#pragma unroll
+    for (int c = 0; c < (FULL ? 1 : KC); ++c) kchunk[c] = FULL || 64 * c + 16 * g < bytes ? krow + 64 * c + 16 * g : none;
+    vchunk = FULL || e0 < bytes ? vrow + e0 : none;
+    vchunk2 = FULL || e1 < bytes ? vrow + e1 : none;
   }
 
   // The table's entry for the tile's row lane % 32 (past the segment: for its last row).
@@ -256,61 +293,67 @@ struct Attend {
   __device__ __forceinline__ uint32_t row_in_page(int at) const {
     return uint32_t(at) - udiv(uint32_t(at), div) * div.d;
   }
-  // A scalar address as it is: the compiler would add the lane's offset to some common part of it ahead of time,
-  // in vector registers; the load instruction takes both.
-  static __device__ __forceinline__ global_bytes scalar(const unsigned char* p) {
-    global_bytes q = (global_bytes)p;
-    asm("" : "+s"(q));
-    return q;
-  }
-  // No load depends on a condition: `entry` past the pool (no page) is taken as page 0, rows past the
-  // end lie on their page all the same.
+  // `entry` past the pool (no page) is taken as page 0; rows past the end lie on their page all the same.
   __device__ __forceinline__ int page_of(int entry) const { return uint32_t(entry) < uint32_t(pool_pages) ? entry : 0; }
+  // A row of the pool for a lane (PAGE < 16); where nothing is to be loaded, the pool's first row for every lane.
+  __device__ __forceinline__ const unsigned char* row_of(const unsigned char* base, int64_t sp, int64_t sr, int pages, int t,
+                                                        int i, bool live) const {
+    const int64_t off = __shfl(pages, i, 64) * sp + row_in_page(t + i) * sr;
+    return base + (live ? off : 0);
+  }
+  __device__ __forceinline__ float load_scale(const float* base, int64_t sp, int64_t sr, int pages, int t, bool live) const {
+    const int64_t off = pages * sp + row_in_page(t + (lane & 31)) * sr;
+    return base[live ? off : 0];
+  }
 
-  __device__ __forceinline__ void load_keys(int entry, int t, Keys& k) const {
+  // The tile at t of table entries `entry`; not live: no memory is read (PAGE 16), or little.
+  __device__ __forceinline__ void load_keys(int entry, int t, bool live, Keys& k) const {
     const int pages = page_of(entry);
-    const uint32_t mine = PAGE16 ? krow : kchunk;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      global_bytes row;
-      if constexpr (PAGE16)
-        row = scalar(k0 + (__builtin_amdgcn_readlane(pages, 16 * u) * kp + row_in_page(t + 16 * u) * kr));
-      else
-        row = (global_bytes)(k0 + (__shfl(pages, 16 * u + r, 64) * kp + row_in_page(t + 16 * u + r) * kr));
+      if constexpr (PAGE == 16) {
+        const Rsrc half = rows_rsrc(k0 + (__builtin_amdgcn_readlane(pages, 16 * u) * kp + row_in_page(t + 16 * u) * kr), live);
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        uint32_t* x = reinterpret_cast<uint32_t*>(&k.x[u][c]);
-        if constexpr (FULL)
-          load_cache<16, false>(row + mine + 64 * c, x);
-        else
-          load_cache<16, false>(row + (mine + (64 * c + 16 * g < key_bytes ? 64 * c : -16 * g)), x);
+        for (int c = 0; c < KC; ++c)
+          load_buffer<16, false>(half, kchunk[FULL ? 0 : c], FULL ? 64 * c : 0, reinterpret_cast<uint32_t*>(&k.x[u][c]));
+      } else {
+        const unsigned char* row = row_of(k0, kp, kr, pages, t, 16 * u + r, live);
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+          load_words<16>(row + (FULL ? kchunk[0] + 64 * c : kchunk[FULL ? 0 : c]), reinterpret_cast<uint32_t*>(&k.x[u][c]));
       }
     }
-    if constexpr (E4M3) k.scale = ks0[pages * ksp + row_in_page(t + (lane & 31)) * ksr];
+    if constexpr (E4M3) k.scale = load_scale(ks0, ksp, ksr, pages, t, live);
   }
 
   // Values are read past the caches: nothing else needs their lines (keys are not, as a line of a
   // key row is covered by two loads).
-  __device__ __forceinline__ void load_values(int entry, int t, Values& v) const {
+  __device__ __forceinline__ void load_values(int entry, int t, bool live, Values& v) const {
     const int pages = page_of(entry);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const unsigned char* half = nullptr;
-      if constexpr (PAGE16) half = v0 + (__builtin_amdgcn_readlane(pages, 16 * u) * vp + row_in_page(t + 16 * u) * vr);
+      if constexpr (PAGE == 16) {
+        const unsigned char* half = v0 + (__builtin_amdgcn_readlane(pages, 16 * u) * vp + row_in_page(t + 16 * u) * vr);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        global_bytes row;
-        if constexpr (PAGE16) {
-          row = scalar(half + j * vr);
-        } else {
-          const int i = 16 * u + 4 * g + j;
-          row = (global_bytes)(v0 + (__shfl(pages, i, 64) * vp + row_in_page(t + i) * vr));
+        for (int j = 0; j < 4; ++j) {
+          const Rsrc row = rows_rsrc(half + j * vr, live);
+          load_buffer<VP, true>(row, vchunk, 0, v.x[4 * u + j]);
+          if constexpr (VB == 32) load_buffer<VP, true>(row, FULL ? vchunk : vchunk2, FULL ? DP / 2 * EB : 0, v.x[4 * u + j] + 4);
         }
-        load_cache<VP, true>(row + vrow, v.x[4 * u + j]);
-        if constexpr (VB == 32) load_cache<VP, true>(FULL ? row + vrow + DP / 2 * EB : row + vrow2, v.x[4 * u + j] + 4);
+      } else {
+        const unsigned char* row = nullptr;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (PAGE == 1 || j == 0)
+            row = row_of(v0, vp, vr, pages, t, 16 * u + 4 * g + j, live);
+          else
+            row += live ? vr : 0;
+          gload<VP, 1>(row + vchunk, v.x[4 * u + j]);
+          if constexpr (VB == 32) gload<VP, 1>(row + vchunk2, v.x[4 * u + j] + 4);
+        }
       }
     }
-    if constexpr (E4M3) v.scale = vs0[pages * vsp + row_in_page(t + (lane & 31)) * vsr];
+    if constexpr (E4M3) v.scale = load_scale(vs0, vsp, vsr, pages, t, live);
   }
 };
 
@@ -331,13 +374,13 @@ __device__ __forceinline__ const AttentionArgs& arguments_again() {
 constexpr int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 // Workgroups a CU holds (the registers they are compiled for): every workgroup of a call runs at once.
 constexpr int resident_workgroups(int dp, bool e4m3, int head_tiles, bool plain) {
-  return dp == 256 ? (e4m3 && plain ? 2 : 1) : head_tiles == 2 || !plain ? 2 : 3;
+  return dp == 256 ? (e4m3 && plain ? 2 : 1) : head_tiles == 1 || plain ? 2 : 1;
 }
 
-template <bool BF16, bool E4M3, int DP, int HT, bool PAGE16, bool FULL>
-__global__ __launch_bounds__(kAttnThreads, resident_workgroups(DP, E4M3, HT, PAGE16 && FULL))
+template <bool BF16, bool E4M3, int DP, int HT, int PAGE, bool FULL>
+__global__ __launch_bounds__(kAttnThreads, resident_workgroups(DP, E4M3, HT, PAGE == 16 && FULL))
 void paged_attention_kernel(AttentionArgs args) {
-  typedef Attend<BF16, E4M3, DP, HT, PAGE16, FULL> A;
+  typedef Attend<BF16, E4M3, DP, HT, PAGE, FULL> A;
   constexpr int KS = A::KS, VF = A::VF;
   constexpr bool VBF = A::VBF;
   __shared__ float merge_ml[kAttnWaves][2][16];
@@ -345,29 +388,40 @@ void paged_attention_kernel(AttentionArgs args) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const AttentionArgs& a = args;
-  const uint32_t pairs = uint32_t(a.heads) * uint32_t(a.head_tiles);
+  const uint32_t run = udiv(blockIdx.x, a.pairs_div), pair = blockIdx.x - run * a.pairs_div.d;
+  const int tile = int(udiv(pair, a.heads_div)), h = int(pair) - tile * int(a.heads_div.d), g0 = tile * 16 * HT;
 
-  // this workgroup's run of units [x, x1), and where it starts: sequence b, pair, unit of the pair
-  const Walk walk = walk_lengths(a);
-  const Cut cut = cut_of(walk.total * pairs, gridDim.x, uint32_t(a.least_units));
-  if (blockIdx.x >= cut.wgs) return;
-  const uint32_t x0 = cut.start(blockIdx.x), x1 = cut.start(blockIdx.x + 1);
-  uint32_t x = x0;
+  // this workgroup's run of units [x0, x1), and where it starts: sequence b, unit of it
   int b, n;
-  uint32_t pair, unit, units;
-  {
-    const int at = __popcll(__ballot(walk.before * pairs <= x && lane * walk.per < a.table.batch)) - 1;
-    uint32_t left = x - uint32_t(__builtin_amdgcn_readlane(int(walk.before), at)) * pairs;
+  uint32_t x0, x1, unit, units;
+  Cut cut;
+  if (!a.parts) {  // nothing is cut: every sequence is one unit
+    cut = cut_of(uint32_t(a.table.batch), uint32_t(a.runs), uint32_t(a.least_units));
+    if (run >= cut.runs) return;
+    x0 = cut.start(run);
+    x1 = cut.start(run + 1);
+    b = int(x0);
+    unit = 0;
+    units = 1;
+    n = __builtin_amdgcn_readfirstlane(paged_len(a.lens, b, a.max_len));
+  } else {
+    const Walk walk = walk_lengths(a);
+    cut = cut_of(walk.total, uint32_t(a.runs), uint32_t(a.least_units));
+    if (!a.parts_of_sequences && pair == 0 && threadIdx.x == 0) a.parts[run].count = 0;
+    if (run >= cut.runs) return;
+    x0 = cut.start(run);
+    x1 = cut.start(run + 1);
+    const int at = __popcll(__ballot(walk.before <= x0 && lane * walk.per < a.table.batch)) - 1;
+    unit = x0 - uint32_t(__builtin_amdgcn_readlane(int(walk.before), at));
     b = at * walk.per;
     for (;; ++b) {
       n = __builtin_amdgcn_readfirstlane(paged_len(a.lens, b, a.max_len));
       units = units_of(n, a.unit);
-      if (left < units * pairs || b + 1 >= a.table.batch) break;
-      left -= units * pairs;
+      if (unit < units || b + 1 >= a.table.batch) break;
+      unit -= units;
     }
-    pair = left / units;
-    unit = left - pair * units;
   }
+  uint32_t x = x0;
 
   A w;
   w.lane = lane, w.r = r, w.g = g;
@@ -376,7 +430,6 @@ void paged_attention_kernel(AttentionArgs args) {
 
   while (x < x1) {
     const uint32_t take = units - unit < x1 - x ? units - unit : x1 - x;
-    const int h = int(udiv(pair, a.tiles_div)), g0 = int(pair - uint32_t(h) * a.tiles_div.d) * 16 * HT;
     const AttentionArgs& a = arguments_again();
     w.pools(a, b, h);
     const int t0 = int(unit * a.unit.d);
@@ -388,7 +441,7 @@ void paged_attention_kernel(AttentionArgs args) {
     int t = t0 + wave * kTile;
     // (a wave without rows, or a sequence without any, has no tile)
     const bool any = t < t1;
-    int entry = 0, next = 0;
+    int entry = 0;
     if (any) entry = w.load_pages(t, t1);
 
     // Q^T: column r is head g0 + 16 ht + r
@@ -409,7 +462,7 @@ void paged_attention_kernel(AttentionArgs args) {
         if (!real || !in) q[ht][s] = u32x4{};
       }
     }
-    const int group = a.group;
+    const int group = a.group, head_dim = a.head_dim;
     const int64_t logit_row = a.logit_row;
     float* logits = a.logits ? a.logits + (int64_t(b) * a.heads + h) * group * logit_row : nullptr;
     f32x4 o[HT][VF];
@@ -422,149 +475,145 @@ void paged_attention_kernel(AttentionArgs args) {
       for (int f = 0; f < VF; ++f) o[ht][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // One tile; with MORE the next one's loads among it.  They are in program order whatever the tile holds, so
-    // that every wait is for a fixed number of younger loads.
-    const auto tile = [&](auto more) {
-      constexpr bool MORE = decltype(more)::value;
-      // S^T
-      f32x4 acc[2][HT];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int ht = 0; ht < HT; ++ht) acc[u][ht] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          u32x4 y;
-          if constexpr (E4M3) {
-            const u32x4& c = k.x[u][s >> 1];
-            const uint32_t w0 = c[(s & 1) * 2], w1 = c[(s & 1) * 2 + 1];
-            y = u32x4{from_e4m3<BF16, false>(w0), from_e4m3<BF16, true>(w0), from_e4m3<BF16, false>(w1),
-                      from_e4m3<BF16, true>(w1)};
-            if (!FULL && 64 * (s >> 1) + 16 * g >= a.head_dim) y = u32x4{};
-          } else {
-            y = k.x[u][s];
-            if (!FULL && 32 * s + 8 * g >= a.head_dim) y = u32x4{};
-          }
-#pragma unroll
-          for (int ht = 0; ht < HT; ++ht) acc[u][ht] = mfma<BF16>(y, q[ht][s], acc[u][ht]);
-        }
-      }
-      // base-2 logits
+    // t: the next tile; the one before it is computed while its loads are on their way
+    bool live = any, have = false;
+    uint64_t missing = 0;  // of the tile computed
+    while (live || have) {
       float s[HT][2][4];
+      if (have) {
+        // S^T
+        f32x4 acc[2][HT];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f = scale_log2e;
-          if constexpr (E4M3) f *= __shfl(k.scale, 16 * u + 4 * g + j, 64);
+          for (int ht = 0; ht < HT; ++ht) acc[u][ht] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int ht = 0; ht < HT; ++ht) s[ht][u][j] = acc[u][ht][j] * f;
-        }
-      const uint64_t missing = w.missing_rows(entry, t, t1);
-      if constexpr (MORE) {
-        entry = next;
-        next = w.load_pages(t + 2 * kStep, t1);
-        w.load_keys(entry, t + kStep, k);
-      }
-
-      float vs[2][4];
-      if constexpr (E4M3) {
+          for (int s = 0; s < KS; ++s) {
+            u32x4 y;
+            if constexpr (E4M3) {
+              const u32x4& c = k.x[u][s >> 1];
+              const uint32_t w0 = c[(s & 1) * 2], w1 = c[(s & 1) * 2 + 1];
+              y = u32x4{from_e4m3<BF16, false>(w0), from_e4m3<BF16, true>(w0), from_e4m3<BF16, false>(w1),
+                        from_e4m3<BF16, true>(w1)};
+              if (PAGE < 16 && !FULL && 64 * (s >> 1) + 16 * g >= head_dim) y = u32x4{};
+            } else {
+              y = k.x[u][s];
+              if (PAGE < 16 && !FULL && 32 * s + 8 * g >= head_dim) y = u32x4{};
+            }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) vs[u][j] = __shfl(v.scale, 16 * u + 4 * g + j, 64);
-      }
-      if (missing) {
-        // rows that do not exist: logits of -infinity, values of 0 (their weight of 0 does not help against a
-        // NaN)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool ok = !(missing >> (16 * u + 4 * g + j) & 1);
-#pragma unroll
-            for (int ht = 0; ht < HT; ++ht) s[ht][u][j] = ok ? s[ht][u][j] : -kInf;
-#pragma unroll
-            for (int i = 0; i < A::VW; ++i) v.x[4 * u + j][i] = ok ? v.x[4 * u + j][i] : 0u;
-            if constexpr (E4M3) vs[u][j] = ok ? vs[u][j] : 0.0f;
-          }
-      }
-      if (logits) {
-#pragma unroll
-        for (int ht = 0; ht < HT; ++ht) {
-          const int head = g0 + 16 * ht + r;
-          if (head < group) {
-            float* row = logits + head * logit_row + t + 4 * g;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              *reinterpret_cast<f32x4*>(row + 16 * u) = f32x4{s[ht][u][0], s[ht][u][1], s[ht][u][2], s[ht][u][3]};
+            for (int ht = 0; ht < HT; ++ht) acc[u][ht] = mfma<BF16>(y, q[ht][s], acc[u][ht]);
           }
         }
-      }
-
-      // online softmax, and P^T in B's layout as two 16-bit parts
-      u32x4 hi[HT], lo[HT];
-#pragma unroll
-      for (int ht = 0; ht < HT; ++ht) {
-        float top = m[ht];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[ht][u][j]);
-        top = __builtin_fmaxf(top, lane_xor<16>(top));
-        top = __builtin_fmaxf(top, lane_xor<32>(top));
-        const float ref = finite(top);
-        if (__ballot(top > m[ht])) {
-          const float shrink = __builtin_amdgcn_exp2f(m[ht] - ref);
-          l[ht] *= shrink;
-#pragma unroll
-          for (int f = 0; f < VF; ++f) o[ht][f] *= shrink;
-          m[ht] = top;
-        }
-        float e[8];
+        // base-2 logits
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            e[4 * u + j] = __builtin_amdgcn_exp2f(s[ht][u][j] - ref);
-            l[ht] += e[4 * u + j];
-            if constexpr (E4M3) e[4 * u + j] *= vs[u][j];
-          }
+            float f = scale_log2e;
+            if constexpr (E4M3) f *= __shfl(k.scale, 16 * u + 4 * g + j, 64);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hi[ht][i] = pack2<VBF>(e[2 * i], e[2 * i + 1]);
-          lo[ht][i] = pack2<VBF>(e[2 * i] - low_half<VBF>(hi[ht][i]), e[2 * i + 1] - high_half<VBF>(hi[ht][i]));
-        }
+            for (int ht = 0; ht < HT; ++ht) s[ht][u][j] = acc[u][ht][j] * f;
+          }
       }
-
-      // O^T += V^T P^T
+      const int now = entry;
+      entry = w.load_pages(t + kStep, t1);
+      w.load_keys(now, t, live, k);
+      if (have) {
+        float vs[2][4];
+        if constexpr (E4M3) {
 #pragma unroll
-      for (int f = 0; f < VF; ++f) {
-        u32x4 y;
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (E4M3) {
-            // bytes f of rows 2 i and 2 i + 1, side by side
-            y[i] = from_e4m3<true, false>(perm(v.x[2 * i + 1][f >> 2], v.x[2 * i][f >> 2],
-                                               uint32_t((f & 3) | ((f & 3) + 4) << 8)));
-          } else {
-            y[i] = perm(v.x[2 * i + 1][f >> 1], v.x[2 * i][f >> 1], f & 1 ? 0x07060302u : 0x05040100u);
+            for (int j = 0; j < 4; ++j) vs[u][j] = __shfl(v.scale, 16 * u + 4 * g + j, 64);
+        }
+        if (missing) {
+          // rows that do not exist: logits of -infinity, values of 0 (their weight of 0 does not help against a
+          // NaN)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool ok = !(missing >> (16 * u + 4 * g + j) & 1);
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) s[ht][u][j] = ok ? s[ht][u][j] : -kInf;
+#pragma unroll
+              for (int i = 0; i < A::VW; ++i) v.x[4 * u + j][i] = ok ? v.x[4 * u + j][i] : 0u;
+              if constexpr (E4M3) vs[u][j] = ok ? vs[u][j] : 0.0f;
+            }
+        }
+        if (logits) {
+#pragma unroll
+          for (int ht = 0; ht < HT; ++ht) {
+            const int head = g0 + 16 * ht + r;
+            if (head < group) {
+              float* row = logits + head * logit_row + (t - kStep) + 4 * g;
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                *reinterpret_cast<f32x4*>(row + 16 * u) = f32x4{s[ht][u][0], s[ht][u][1], s[ht][u][2], s[ht][u][3]};
+            }
           }
         }
+
+        // online softmax, and P^T in B's layout as two 16-bit parts
+        u32x4 hi[HT], lo[HT];
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
-          o[ht][f] = mfma<VBF>(y, hi[ht], o[ht][f]);
-          o[ht][f] = mfma<VBF>(y, lo[ht], o[ht][f]);
+          float top = m[ht];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[ht][u][j]);
+          top = max_of_groups(top);
+          const float ref = finite(top);
+          if (__ballot(top > m[ht])) {
+            const float shrink = __builtin_amdgcn_exp2f(m[ht] - ref);
+            l[ht] *= shrink;
+#pragma unroll
+            for (int f = 0; f < VF; ++f) o[ht][f] *= shrink;
+            m[ht] = top;
+          }
+          float e[8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              e[4 * u + j] = __builtin_amdgcn_exp2f(s[ht][u][j] - ref);
+              l[ht] += e[4 * u + j];
+              if constexpr (E4M3) e[4 * u + j] *= vs[u][j];
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            hi[ht][i] = pack2<VBF>(e[2 * i], e[2 * i + 1]);
+            lo[ht][i] = pack2<VBF>(e[2 * i] - low_half<VBF>(hi[ht][i]), e[2 * i + 1] - high_half<VBF>(hi[ht][i]));
+          }
+        }
+
+        // O^T += V^T P^T
+#pragma unroll
+        for (int f = 0; f < VF; ++f) {
+          u32x4 y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (E4M3) {
+              // bytes f of rows 2 i and 2 i + 1, side by side
+              y[i] = from_e4m3<true, false>(perm(v.x[2 * i + 1][f >> 2], v.x[2 * i][f >> 2],
+                                                 uint32_t((f & 3) | ((f & 3) + 4) << 8)));
+            } else {
+              y[i] = perm(v.x[2 * i + 1][f >> 1], v.x[2 * i][f >> 1], f & 1 ? 0x07060302u : 0x05040100u);
+            }
+          }
+#pragma unroll
+          for (int ht = 0; ht < HT; ++ht) {
+            o[ht][f] = mfma<VBF>(y, hi[ht], o[ht][f]);
+            o[ht][f] = mfma<VBF>(y, lo[ht], o[ht][f]);
+          }
         }
       }
-      if constexpr (MORE) w.load_values(entry, t + kStep, v);
-    };
-    if (any) {
-      next = w.load_pages(t + kStep, t1);
-      w.load_keys(entry, t, k);
-      w.load_values(entry, t, v);
-      for (; t + kStep < t1; t += kStep) tile(std::true_type());
-      tile(std::false_type());
+      w.load_values(now, t, live, v);
+      missing = w.missing_rows(now, t, t1);
+      have = live;
+      t += kStep;
+      live = t < t1;
     }
 
     // the four waves' parts of each 16 heads
@@ -575,8 +624,7 @@ void paged_attention_kernel(AttentionArgs args) {
     const int64_t slot = (int64_t(blockIdx.x) * 2 + (x != x0)) * (16 * HT);
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
-      l[ht] += lane_xor<16>(l[ht]);
-      l[ht] += lane_xor<32>(l[ht]);
+      l[ht] = sum_of_groups(l[ht]);
       __syncthreads();  // the last parts have been read
       if (g == 0) {
         merge_ml[wave][0][r] = m[ht];
@@ -630,125 +678,127 @@ void paged_attention_kernel(AttentionArgs args) {
       }
     }
 
+    if (e.parts && unit == 0 && pair == 0 && tid == 0 && (e.parts_of_sequences || !done)) {
+      // the sequence starts in this run: the runs up to its last unit have its other parts
+      const int count = done ? 0 : int(cut.owner(x + units - 1) - run) + 1;
+      e.parts[e.parts_of_sequences ? b : int(run)] = PagedParts{b, int32_t(run), count, x != x0};
+    }
     x += take;
     unit += take;
-    if (unit == units) {
+    if (unit == units && x < x1) {
       unit = 0;
-      if (++pair == pairs) {
-        pair = 0;
-        ++b;
-        if (x < x1) {
-          n = __builtin_amdgcn_readfirstlane(paged_len(e.lens, b, e.max_len));
-          units = units_of(n, e.unit);
-        }
-      }
+      ++b;
+      n = __builtin_amdgcn_readfirstlane(paged_len(e.lens, b, e.max_len));
+      units = units_of(n, e.unit);
     }
   }
 }
 
-// The parts of one query head of a pair that was cut, joined: their maxima give each part's factor,
-// sums and outputs are added in a fixed order.  One workgroup a (sequence, query head): 32 lanes of four or eight
-// elements, 16 parts at a time.
+// The parts of one query head of a sequence that was cut, joined: their maxima give each part's factor, sums and
+// outputs are added in a fixed order.  Grid: (sequence or run, query head); those with nothing to join end at
+// once.  32 lanes of four or eight elements, 8 parts at a time and 8 such rounds of loads on their way: the call's
+// time is three trips to memory.
 template <bool BF16>
-__global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(AttentionArgs a, uint32_t grid, Div32 q_heads) {
-  constexpr int G = kJoinThreads / 32;
+__global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(AttentionArgs a) {
+  constexpr int G = kJoinThreads / 32, R = 64 / G;
   __shared__ float part[G][kPagedMaxHeadDim];
-  __shared__ float sums[G];
-  const int b = int(udiv(blockIdx.x, q_heads)), hh = int(blockIdx.x) - b * int(q_heads.d);
-  const uint32_t h = uint32_t(hh) / uint32_t(a.group), in_group = uint32_t(hh) - h * uint32_t(a.group);
-  const uint32_t pairs = uint32_t(a.heads) * uint32_t(a.head_tiles), tile = in_group / uint32_t(a.tile_heads);
-  const int n = __builtin_amdgcn_readfirstlane(paged_len(a.lens, b, a.max_len));
-  const uint32_t units = units_of(n, a.unit);
-  const Walk walk = walk_lengths(a);
-  const Cut cut = cut_of(walk.total * pairs, grid, uint32_t(a.least_units));
-  uint32_t before = uint32_t(__builtin_amdgcn_readlane(int(walk.before), b / walk.per));
-  for (int k = b / walk.per * walk.per; k < b; ++k) before += units_of(paged_len(a.lens, k, a.max_len), a.unit);
-  const uint32_t x0 = before * pairs + (h * uint32_t(a.head_tiles) + tile) * units;
-  const uint32_t i0 = cut.owner(x0), i1 = cut.owner(x0 + units - 1);
-  if (i0 == i1) return;
-  // part k: of workgroup i0 + k, in its second slot where its run does not start with this pair
-  const int parts = int(i1 - i0) + 1, first_slot = cut.start(i0) == x0 ? 0 : 1;
-  const int64_t row0 = in_group - tile * uint32_t(a.tile_heads);
-  const auto row = [&](int k) { return (int64_t(i0 + k) * 2 + (k == 0 ? first_slot : 0)) * a.tile_heads + row0; };
+  const PagedParts p = a.parts[blockIdx.x];
+  if (p.count == 0) return;
+  const int hh = int(blockIdx.y), h = hh / a.group, in_group = hh - h * a.group, tile = in_group / a.tile_heads;
+  // part k: of run p.run + k, in its second slot where its run did not start with this sequence
+  const int64_t step = int64_t(a.pairs_div.d) * 2 * a.tile_heads;
+  const int64_t row0 = (int64_t(p.run) * a.pairs_div.d + tile * a.heads + h) * 2 * a.tile_heads + (in_group - tile * a.tile_heads);
+  const int64_t first = p.slot ? a.tile_heads : 0;
+  const int lane = threadIdx.x & 63, lane4 = threadIdx.x & 31, grp = threadIdx.x >> 5;
   float top = -kInf;
-  for (int k = threadIdx.x & 63; k < parts; k += 64) top = __builtin_fmaxf(top, a.part_ml[2 * row(k)]);
+  for (int k = lane; k < p.count; k += 64) top = __builtin_fmaxf(top, a.part_ml[2 * (row0 + k * step + (k ? 0 : first))]);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d, 64));
   const float ref = finite(top);
-  const int lane4 = threadIdx.x & 31, grp = threadIdx.x >> 5;
   f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int k = grp; k < parts; k += G) {
-    const int64_t at = row(k);
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
-    sum += a.part_ml[2 * at + 1] * f;
+  float total = 0.0f;
+  for (int k0 = 0; k0 < p.count; k0 += 64) {
+    // lane k: the factor of part k0 + k
+    float f = 0.0f;
+    if (k0 + lane < p.count) {
+      const float* ml = a.part_ml + 2 * (row0 + (k0 + lane) * step + (k0 + lane ? 0 : first));
+      f = __builtin_amdgcn_exp2f(ml[0] - ref);
+      total += ml[1] * f;
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int d = 4 * lane4 + 128 * c;
-      if (d < a.head_dim) acc[c] += *reinterpret_cast<const f32x4*>(a.part_o + at * a.head_dim + d) * f;
+      if (128 * c >= a.head_dim) break;
+      // lanes past the row read its end again and stay for the exchanges
+      const int d = 4 * lane4 + 128 * c < a.head_dim ? 4 * lane4 + 128 * c : a.head_dim - 4;
+      const auto load = [&](int i) {
+        const int k = k0 + grp + G * i, at = k < p.count ? k : p.count - 1;
+        return *reinterpret_cast<const f32x4*>(a.part_o + (row0 + at * step + (at ? 0 : first)) * a.head_dim + d);
+      };
+      const auto add = [&](int i, const f32x4& x) {
+        const float y = __shfl(f, grp + G * i, 64);
+        if (k0 + grp + G * i < p.count) acc[c] += x * y;
+      };
+      if (p.count <= G) {
+        add(0, load(0));
+      } else {
+        f32x4 x[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i] = load(i);
+#pragma unroll
+        for (int i = 0; i < R; ++i) add(i, x[i]);
+      }
     }
   }
 #pragma unroll
+  for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d, 64);
+#pragma unroll
   for (int c = 0; c < 2; ++c) *reinterpret_cast<f32x4*>(&part[grp][4 * lane4 + 128 * c]) = acc[c];
-  if (lane4 == 0) sums[grp] = sum;
   __syncthreads();
   const int d = threadIdx.x;
   if (d >= a.head_dim) return;
-  float total = 0.0f, y = 0.0f;
+  float y = 0.0f;
 #pragma unroll
-  for (int k = 0; k < G; ++k) {
-    total += sums[k];
-    y += part[k][d];
-  }
+  for (int k = 0; k < G; ++k) y += part[k][d];
   y = total == 0.0f ? 0.0f : y * (1.0f / total);
-  reinterpret_cast<uint16_t*>(a.out + b * a.ob + hh * a.oh)[d] = uint16_t(pack2<BF16>(y, 0.0f));
+  reinterpret_cast<uint16_t*>(a.out + p.b * a.ob + hh * a.oh)[d] = uint16_t(pack2<BF16>(y, 0.0f));
   if (d == 0) {
-    if (a.lse) a.lse[b * a.lb + hh * a.lh] = (top + __builtin_amdgcn_logf(total)) * 0.6931471805599453f;
+    if (a.lse) a.lse[p.b * a.lb + hh * a.lh] = (top + __builtin_amdgcn_logf(total)) * 0.6931471805599453f;
     if (a.final_ml) {
-      a.final_ml[2 * int64_t(blockIdx.x)] = top;
-      a.final_ml[2 * int64_t(blockIdx.x) + 1] = total;
+      float* ml = a.final_ml + 2 * (int64_t(p.b) * a.heads * a.group + hh);
+      ml[0] = top;
+      ml[1] = total;
     }
   }
 }
 
 // weights_out[i] = weights[i] + the sum over a cache head's query heads of exp2(logit - maximum) / sum.
-// One workgroup a kWeightRows rows of one (sequence, cache head).
-constexpr int kWeightRows = 1024;
-__global__ __launch_bounds__(256) void paged_weights_kernel(AttentionArgs a, Div32 heads, Div32 chunks) {
+// One lane a row, one workgroup 256 rows of one (sequence, cache head).  Bound: the logits' bytes.
+constexpr int kWeightRows = 256;
+__global__ __launch_bounds__(kWeightRows) void paged_weights_kernel(AttentionArgs a, Div32 heads, Div32 chunks) {
   const uint32_t bh = udiv(blockIdx.x, chunks), chunk = blockIdx.x - bh * chunks.d;
   const int b = int(udiv(bh, heads)), h = int(bh - uint32_t(b) * heads.d);
   const int n = paged_len(a.lens, b, a.max_len);
-  const int i0 = int(chunk) * kWeightRows;
-  if (i0 >= n) return;
-  const float* w = a.weights + b * a.w.sb + h * a.w.sh;
-  float* wo = a.weights_out + b * a.wo.sb + h * a.wo.sh;
-  float sum[kWeightRows / 256] = {};
+  const int i = int(chunk) * kWeightRows + int(threadIdx.x);
+  if (i >= n) return;
+  const float before = a.weights[b * a.w.sb + h * a.w.sh + i * a.w.sc];
+  const float* ml = a.final_ml + 2 * int64_t(bh) * a.group;
+  const float* x = a.logits + int64_t(bh) * a.group * a.logit_row + i;
+  float sum = 0.0f;
+#pragma unroll 4
   for (int g = 0; g < a.group; ++g) {
-    const int64_t hq = int64_t(bh) * a.group + g;
-    const float ref = finite(a.final_ml[2 * hq]), total = a.final_ml[2 * hq + 1];
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    const float* x = a.logits + hq * a.logit_row;
-#pragma unroll
-    for (int k = 0; k < kWeightRows / 256; ++k) {
-      const int i = i0 + 256 * k + int(threadIdx.x);
-      if (i < n) sum[k] += __builtin_amdgcn_exp2f(x[i] - ref) * inv;
-    }
+    const float total = ml[2 * g + 1], inv = total == 0.0f ? 0.0f : 1.0f / total;
+    sum += __builtin_amdgcn_exp2f(x[g * a.logit_row] - finite(ml[2 * g])) * inv;
   }
-#pragma unroll
-  for (int k = 0; k < kWeightRows / 256; ++k) {
-    const int i = i0 + 256 * k + int(threadIdx.x);
-    if (i < n) wo[i * a.wo.sc] = w[i * a.w.sc] + sum[k];
-  }
+  a.weights_out[b * a.wo.sb + h * a.wo.sh + i * a.wo.sc] = before + sum;
 }
 
-template <bool BF16, bool E4M3, int DP, int HT, bool PAGE16, bool FULL>
+template <bool BF16, bool E4M3, int DP, int HT, int PAGE, bool FULL>
 void attend(const AttentionArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((paged_attention_kernel<BF16, E4M3, DP, HT, PAGE16, FULL>), dim3(uint32_t(a.workgroups)),
+  hipLaunchKernelGGL((paged_attention_kernel<BF16, E4M3, DP, HT, PAGE, FULL>), dim3(uint32_t(a.workgroups)),
                      dim3(kAttnThreads), 0, s, a);
 }
 
-// PAGE16's lane offsets are 32-bit: 16 rows of either pool have to fit.
+// PAGE 16's lane offsets are 32-bit: 16 rows of either pool have to fit.
 bool pages_of_16(const PagedPool& p) {
   const int64_t most = int64_t(1) << 27;
   return p.page_size % 16 == 0 && p.kr < most && p.vr < most;
@@ -756,8 +806,10 @@ bool pages_of_16(const PagedPool& p) {
 
 template <bool BF16, bool E4M3, int DP, int HT>
 void by_page(const AttentionArgs& a, hipStream_t s) {
-  if (!pages_of_16(a.pool)) return attend<BF16, E4M3, DP, HT, false, false>(a, s);
-  return a.head_dim == DP ? attend<BF16, E4M3, DP, HT, true, true>(a, s) : attend<BF16, E4M3, DP, HT, true, false>(a, s);
+  const bool full = a.head_dim == DP;
+  if (pages_of_16(a.pool)) return full ? attend<BF16, E4M3, DP, HT, 16, true>(a, s) : attend<BF16, E4M3, DP, HT, 16, false>(a, s);
+  if (a.pool.page_size % 4 == 0) return full ? attend<BF16, E4M3, DP, HT, 4, true>(a, s) : attend<BF16, E4M3, DP, HT, 4, false>(a, s);
+  return attend<BF16, E4M3, DP, HT, 1, false>(a, s);
 }
 
 template <bool BF16, bool E4M3, int DP>
@@ -778,23 +830,27 @@ void by_dim(const AttentionArgs& a, hipStream_t s) {
 
 int64_t paged_logit_row(int64_t max_len) { return (max_len + dev::kStep - 1) / dev::kStep * dev::kStep; }
 
+static int64_t runs_of(int64_t units, int64_t least, int64_t pairs, int64_t resident) {
+  const int64_t fit = std::max<int64_t>(1, (resident * dev::kCus + pairs / 2) / pairs);
+  return std::min((units + least - 1) / least, fit);
+}
+
 PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len) {
   PagedCut c{};
   // 32 heads at once for larger groups, where their outputs fit the registers
   c.tile_heads = group > 16 && head_dim <= 128 ? 32 : 16;
   c.head_tiles = (group + c.tile_heads - 1) / c.tile_heads;
-  const int64_t pairs = batch * heads * c.head_tiles;
   c.unit_rows = dev::kStep;
   c.least_units = 2;
   if (max_len <= 512) {
     c.unit_rows = std::max<int64_t>(dev::kStep, (max_len + dev::kStep - 1) / dev::kStep * dev::kStep);
     c.least_units = 1;
   }
-  const int64_t most = pairs * std::max<int64_t>(1, (max_len + c.unit_rows - 1) / c.unit_rows);
-  c.cuts = most > pairs;
-  const int64_t resident = dev::resident_workgroups(dev::padded_dim(int(head_dim)), true, int(c.tile_heads / 16), true);
-  c.workgroups = std::min<int64_t>((most + c.least_units - 1) / c.least_units, resident * dev::kCus);
-  c.units = most;
+  c.units = batch * std::max<int64_t>(1, (max_len + c.unit_rows - 1) / c.unit_rows);
+  c.cuts = c.units > batch;
+  const int64_t pairs = heads * c.head_tiles;
+  c.runs = runs_of(c.units, c.least_units, pairs, dev::resident_workgroups(dev::padded_dim(int(head_dim)), true, int(c.tile_heads / 16), true));
+  c.workgroups = c.runs * pairs;
   return c;
 }
 
@@ -805,23 +861,28 @@ int launch_paged_attention(const AttentionArgs& in, int dtype, int cache_dtype, 
   const int64_t chunks = (int64_t(a.max_len) + dev::kWeightRows - 1) / dev::kWeightRows;
   if (rows * chunks >= int64_t(1) << 31) return TC_E_RANGE;
   const int dp = dev::padded_dim(a.head_dim);
-  a.workgroups = std::min(a.workgroups, dev::kCus * dev::resident_workgroups(dp, cache_dtype == TC_E4M3, a.tile_heads / 16,
-                                                                             dev::pages_of_16(a.pool) && a.head_dim == dp));
+  const int64_t pairs = int64_t(a.heads) * a.head_tiles;
+  a.runs = int32_t(runs_of(a.units, a.least_units, pairs,
+                           dev::resident_workgroups(dp, cache_dtype == TC_E4M3, a.tile_heads / 16,
+                                                    dev::pages_of_16(a.pool) && a.head_dim == dp)));
+  a.workgroups = int32_t(a.runs * pairs);
+  a.pairs_div = make_div32(uint32_t(pairs));
+  a.heads_div = make_div32(uint32_t(a.heads));
+  a.parts_of_sequences = a.table.batch <= a.runs;
   const bool bf16 = dtype == TC_BF16, e4m3 = cache_dtype == TC_E4M3;
   if (bf16)
     e4m3 ? dev::by_dim<true, true>(a, s) : dev::by_dim<true, false>(a, s);
   else
     e4m3 ? dev::by_dim<false, true>(a, s) : dev::by_dim<false, false>(a, s);
-  if (a.part_o) {
-    const uint32_t hq = uint32_t(rows) * uint32_t(a.group);
-    const Div32 qh = make_div32(uint32_t(a.heads) * uint32_t(a.group));
+  if (a.parts) {
+    const dim3 grid(uint32_t(std::min(a.table.batch, a.runs)), uint32_t(a.heads) * uint32_t(a.group));
     if (bf16)
-      hipLaunchKernelGGL(dev::paged_join_kernel<true>, dim3(hq), dim3(dev::kJoinThreads), 0, s, a, uint32_t(a.workgroups), qh);
+      hipLaunchKernelGGL(dev::paged_join_kernel<true>, grid, dim3(dev::kJoinThreads), 0, s, a);
     else
-      hipLaunchKernelGGL(dev::paged_join_kernel<false>, dim3(hq), dim3(dev::kJoinThreads), 0, s, a, uint32_t(a.workgroups), qh);
+      hipLaunchKernelGGL(dev::paged_join_kernel<false>, grid, dim3(dev::kJoinThreads), 0, s, a);
   }
   if (a.weights_out && chunks > 0)
-    hipLaunchKernelGGL(dev::paged_weights_kernel, dim3(uint32_t(rows * chunks)), dim3(256), 0, s, a,
+    hipLaunchKernelGGL(dev::paged_weights_kernel, dim3(uint32_t(rows * chunks)), dim3(dev::kWeightRows), 0, s, a,
                        make_div32(uint32_t(a.heads)), make_div32(uint32_t(chunks)));
   return TC_OK;
 }
