@@ -379,6 +379,7 @@ class PagedCache:
     __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_c", "_ref", "device")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
+        _import_torch()
         self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
         if k.dtype != v.dtype:
             raise ValueError(f"keys are {k.dtype}, values {v.dtype}")
@@ -391,7 +392,7 @@ class PagedCache:
             if (x is not None) != (c.dtype == TC_E4M3):
                 raise ValueError("8-bit caches have k_scale and v_scale, others have none")
             if x is not None:
-                _want(name, x, "float32")
+                _want(name, x, _T_F32)
                 setattr(c, name, x.data_ptr())
                 setattr(c, name + "_layout", make_layout(x.shape, x.stride()))
         _device_of(self, v, k_scale, v_scale)
@@ -408,15 +409,31 @@ class PagedCache:
     head_dim = property(lambda self: self._k.shape[3])
 
 
+_torch = None
+_T_I32 = _T_F32 = None
+_PAGED_DTYPES = {}
+
+
+def _import_torch():
+    """torch and the types the paged entry points name, looked up once."""
+    global _torch, _T_I32, _T_F32
+    if _torch is None:
+        import torch
+        _T_I32, _T_F32 = torch.int32, torch.float32
+        _PAGED_DTYPES.update({torch.float16: TC_F16, torch.bfloat16: TC_BF16, torch.float8_e4m3fn: TC_E4M3})
+        _torch = torch
+    return _torch
+
+
 def _paged_dtype(x) -> int:
-    name = str(x.dtype)[6:]
-    if name not in ("float16", "bfloat16", "float8_e4m3fn"):
+    code = _PAGED_DTYPES.get(x.dtype)
+    if code is None:
         raise ValueError(f"expected float16, bfloat16 or (a cache) float8_e4m3fn, got {x.dtype}")
-    return DTYPE_BY_NAME[name]
+    return code
 
 
-def _want(name: str, x, dtype: str) -> None:
-    if str(x.dtype)[6:] != dtype:
+def _want(name: str, x, dtype) -> None:
+    if x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
 
 
@@ -429,12 +446,13 @@ def _device_of(cache, *tensors):
 
 
 def _vector(name: str, x, n: int) -> int:
-    _want(name, x, "int32")
-    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+    _want(name, x, _T_I32)
+    if x.shape != (n,) or (n > 1 and x.stride() != (1,)):
         raise ValueError(f"{name} must be contiguous with {n} elements")
     return x.data_ptr()
 
 
+_NONE = (None, None)
 _layout_cache = {}
 
 
@@ -450,36 +468,32 @@ def _lay(x):
     return at
 
 
-class _Launch:
-    """The tensors' device made current, and the stream the call goes to."""
+def _enter(dev):
+    """Makes the tensors' device current; returns the one to go back to, or None."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not {dev}")
+    here = _torch.cuda.current_device()
+    if here == dev.index:
+        return None
+    _torch.cuda.set_device(dev)
+    return here
 
-    __slots__ = ("dev", "prev", "stream", "handle")
 
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.prev = dev, stream, None
+def _paged_stream(dev, stream) -> int:
+    if stream is not None:
+        return _stream(stream)
+    try:
+        return _torch._C._cuda_getCurrentRawStream(dev.index)  # 0.1 us; current_stream() takes 2.5
+    except AttributeError:
+        return _torch.cuda.current_stream().cuda_stream
 
-    def __enter__(self):
-        import torch
-        if self.dev.type != "cuda":
-            raise ValueError(f"tensors must be on a GPU, not {self.dev}")
-        if torch.cuda.current_device() != self.dev.index:
-            self.prev = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-        self.handle = torch.cuda.current_stream().cuda_stream if self.stream is None else _stream(self.stream)
-        return self
 
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            import torch
-            torch.cuda.set_device(self.prev)
-
-    def empty(self, n: int, dtype, shape=None):
-        """Memory for this call, allocated on its stream: another stream's next use waits its turn."""
-        import torch
-        if self.stream is None or self.handle == torch.cuda.current_stream().cuda_stream:
-            return torch.empty(shape or n, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=self.dev)):
-            return torch.empty(shape or n, dtype=dtype, device=self.dev)
+def _empty_on(handle, stream, dev, shape, dtype):
+    """Memory for this call, allocated on its stream: another stream's next use of it waits its turn."""
+    if stream is None or handle == _torch.cuda.current_stream().cuda_stream:
+        return _torch.empty(shape, dtype=dtype, device=dev)
+    with _torch.cuda.stream(_torch.cuda.ExternalStream(handle, device=dev)):
+        return _torch.empty(shape, dtype=dtype, device=dev)
 
 
 def tc_paged_append(cache: PagedCache, k, v, block_table, seq_lens, token_starts=None, weights=None,
@@ -491,22 +505,28 @@ def tc_paged_append(cache: PagedCache, k, v, block_table, seq_lens, token_starts
     rows after the append.  Token b becomes the last row of sequence b; with ``token_starts`` (batch + 1) int32,
     tokens starts[b] .. starts[b + 1] - 1 become its last rows and tokens past starts[batch] are padding.
     ``weights`` (batch, heads, capacity) float32, if given, is zeroed for the new rows."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _device_of(cache, k, v, block_table, seq_lens, token_starts, weights)
     if k.dtype != v.dtype:
         raise ValueError(f"keys are {k.dtype}, values {v.dtype}")
-    _want("block_table", block_table, "int32")
+    _want("block_table", block_table, _T_I32)
     batch = block_table.shape[0]
     lens = _vector("seq_lens", seq_lens, batch)
     starts = None if token_starts is None else _vector("token_starts", token_starts, batch + 1)
+    wl, wp = _NONE, None
     if weights is not None:
-        _want("weights", weights, "float32")
+        _want("weights", weights, _T_F32)
+        wl, wp = _lay(weights), weights.data_ptr()
     kl, vl, tl = _lay(k), _lay(v), _lay(block_table)
-    wl = (None, None) if weights is None else _lay(weights)
-    with _Launch(dev, stream) as at:
-        _check(lib.tc_paged_append(cache._ref, k.data_ptr(), kl[0], v.data_ptr(), vl[0], _paged_dtype(k),
-                                   block_table.data_ptr(), tl[0], lens, starts,
-                                   None if weights is None else weights.data_ptr(), wl[0], at.handle))
+    back = _enter(dev)
+    try:
+        rc = lib.tc_paged_append(cache._ref, k.data_ptr(), kl[0], v.data_ptr(), vl[0], _paged_dtype(k),
+                                 block_table.data_ptr(), tl[0], lens, starts, wp, wl[0], _paged_stream(dev, stream))
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != TC_OK:
+        _check(rc)
 
 
 def tc_paged_attention(q, cache: PagedCache, block_table, seq_lens, scale: Optional[float] = None,
@@ -518,45 +538,52 @@ def tc_paged_attention(q, cache: PagedCache, block_table, seq_lens, scale: Optio
     hold); a tight bound saves launches and memory.  ``lse`` (batch, q_heads) float32 receives the log of the
     sums.  ``weights`` (batch, heads, capacity) float32: ``weights_out`` (default: ``weights`` itself) receives
     weights plus each row's attention weight summed over the query heads of its cache head."""
-    import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _device_of(cache, q, block_table, seq_lens, out, lse, weights, weights_out)
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be (batch, q_heads, head_dim), block_table (batch, columns)")
-    _want("block_table", block_table, "int32")
+    _want("block_table", block_table, _T_I32)
     batch, q_heads, dim = q.shape
     lens = _vector("seq_lens", seq_lens, batch)
     if max_len is None:
         max_len = block_table.shape[1] * cache.page_size
     if scale is None:
         scale = dim ** -0.5
-    if weights_out is None:
-        weights_out = weights
-    elif weights is None:
+    ll, wl, wol = _NONE, _NONE, _NONE
+    lp = wp = wop = None
+    if lse is not None:
+        _want("lse", lse, _T_F32)
+        ll, lp = _lay(lse), lse.data_ptr()
+    if weights is not None:
+        if weights_out is None:
+            weights_out = weights
+        _want("weights", weights, _T_F32)
+        _want("weights_out", weights_out, _T_F32)
+        wl, wol, wp, wop = _lay(weights), _lay(weights_out), weights.data_ptr(), weights_out.data_ptr()
+    elif weights_out is not None:
         raise ValueError("weights_out without weights")
-    for name, x in (("lse", lse), ("weights", weights), ("weights_out", weights_out)):
-        if x is not None:
-            _want(name, x, "float32")
+    code = _paged_dtype(q)
     ql, tl = _lay(q), _lay(block_table)
-    none = (None, None)
-    ll = none if lse is None else _lay(lse)
-    wl, wol = (none, none) if weights is None else (_lay(weights), _lay(weights_out))
-    with _Launch(dev, stream) as at:
+    back = _enter(dev)
+    try:
+        handle = _paged_stream(dev, stream)
         if out is None:
-            out = at.empty(0, q.dtype, q.shape)
+            out = _empty_on(handle, stream, dev, q.shape, q.dtype)
         elif out.dtype != q.dtype:
             raise ValueError(f"out is {out.dtype}, q {q.dtype}")
         ol = _lay(out)
         need = lib.tc_paged_attention_workspace(batch, q_heads, cache.heads, dim, max_len, weights is not None)
         if need < 0:
-            _check(int(need))
-        work = at.empty(need, torch.uint8) if need else None
-        _check(lib.tc_paged_attention(
-            cache._ref, q.data_ptr(), ql[0], out.data_ptr(), ol[0], _paged_dtype(q), block_table.data_ptr(), tl[0], lens,
-            max_len, scale, None if lse is None else lse.data_ptr(), ll[0],
-            None if weights is None else weights.data_ptr(), wl[0],
-            None if weights_out is None else weights_out.data_ptr(), wol[0],
-            None if work is None else work.data_ptr(), need, at.handle))
+            _check(need)
+        work = _empty_on(handle, stream, dev, need, _torch.uint8) if need else None
+        rc = lib.tc_paged_attention(cache._ref, q.data_ptr(), ql[0], out.data_ptr(), ol[0], code, block_table.data_ptr(), tl[0],
+                                    lens, max_len, scale, lp, ll[0], wp, wl[0], wop, wol[0],
+                                    None if work is None else work.data_ptr(), need, handle)
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != TC_OK:
+        _check(rc)
     return out
 
 
@@ -568,28 +595,37 @@ def tc_paged_evict(src: PagedCache, block_table, seq_lens, weights, dst: PagedCa
     in ``dst`` (another pool, or pages of the same one that hold none of the kept rows).  Returns
     ``(lens_out, kept)``: the new lengths, and the rows kept, (batch, heads, min(budget, max_len)) int32 with -1
     past the new length.  ``weights_out`` receives the kept rows' weights."""
-    import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _device_of(src, block_table, seq_lens, weights, dst, dst_table, lens_out, weights_out, kept)
     if block_table.dim() != 2:
         raise ValueError("block_table must be (batch, columns)")
     batch = block_table.shape[0]
-    for name, x, dtype in (("block_table", block_table, "int32"), ("dst_table", dst_table, "int32"),
-                           ("weights", weights, "float32"), ("kept", kept, "int32"), ("weights_out", weights_out, "float32")):
-        if x is not None:
-            _want(name, x, dtype)
+    _want("block_table", block_table, _T_I32)
+    _want("dst_table", dst_table, _T_I32)
+    _want("weights", weights, _T_F32)
     lens = _vector("seq_lens", seq_lens, batch)
     held = block_table.shape[1] * src.page_size
     max_len = held if max_len is None else min(max_len, held)
-    with _Launch(dev, stream) as at:
+    wol, wop = _NONE, None
+    if weights_out is not None:
+        _want("weights_out", weights_out, _T_F32)
+        wol, wop = _lay(weights_out), weights_out.data_ptr()
+    tl, wl, dl = _lay(block_table), _lay(weights), _lay(dst_table)
+    back = _enter(dev)
+    try:
+        handle = _paged_stream(dev, stream)
         if lens_out is None:
-            lens_out = at.empty(batch, torch.int32)
+            lens_out = _empty_on(handle, stream, dev, batch, _T_I32)
         if kept is None:
-            kept = at.empty(0, torch.int32, (batch, src.heads, max(0, min(budget, max_len))))
-        tl, wl, dl, kl = _lay(block_table), _lay(weights), _lay(dst_table), _lay(kept)
-        wol = (None, None) if weights_out is None else _lay(weights_out)
-        _check(lib.tc_paged_evict(src._ref, block_table.data_ptr(), tl[0], lens, max_len, weights.data_ptr(), wl[0],
-                                  dst._ref, dst_table.data_ptr(), dl[0], budget, recent,
-                                  _vector("lens_out", lens_out, batch), kept.data_ptr(), kl[0],
-                                  None if weights_out is None else weights_out.data_ptr(), wol[0], at.handle))
+            kept = _empty_on(handle, stream, dev, (batch, src.heads, max(0, min(budget, max_len))), _T_I32)
+        _want("kept", kept, _T_I32)
+        kl = _lay(kept)
+        rc = lib.tc_paged_evict(src._ref, block_table.data_ptr(), tl[0], lens, max_len, weights.data_ptr(), wl[0],
+                                dst._ref, dst_table.data_ptr(), dl[0], budget, recent,
+                                _vector("lens_out", lens_out, batch), kept.data_ptr(), kl[0], wop, wol[0], handle)
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != TC_OK:
+        _check(rc)
     return lens_out, kept

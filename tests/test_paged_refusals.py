@@ -37,8 +37,8 @@ def _append(cache=None, dtype=L.TC_BF16, new=(3, HEADS, DIM), k=BASE + (4 << 20)
 
 
 def _attend(cache=None, dtype=L.TC_BF16, q=BASE + (4 << 20), q_shape=(3, 4, DIM), out=BASE + (5 << 20), out_shape=None, table=(3, 4),
-            max_len=64, scale=1.0, lse=None, lse_shape=(3, 4), w=None, wo=None, w_shape=(3, HEADS, 64), work=BASE + (9 << 20),
-            work_bytes=1 << 20, out_stride=None, lens=BASE + (7 << 20)):
+            max_len=64, scale=1.0, lse=None, lse_shape=(3, 4), w=None, wo=None, w_shape=(3, HEADS, 64), work=BASE + (256 << 20),
+            work_bytes=1 << 26, out_stride=None, lens=BASE + (7 << 20)):
     cache = _cache() if cache is None else cache
     ql, ol, tl, ll, wl = _lay(q_shape), _lay(out_shape or q_shape, out_stride), _lay(table), _lay(lse_shape), _lay(w_shape)
     return L.load_library().tc_paged_attention(_ref(cache), q, _ref(ql), out, _ref(ol), dtype, BASE + (6 << 20), _ref(tl), lens, max_len,
@@ -99,7 +99,7 @@ BIG = 1 << 59
     (L.TC_E_RANGE, "max_len", lambda: _attend(max_len=-1)),
     (L.TC_E_ARG, "workspace", lambda: _attend(table=(3, 400), max_len=6000, work_bytes=64)),
     (L.TC_E_NULL, "workspace", lambda: _attend(table=(3, 400), max_len=6000, work=None)),
-    (L.TC_E_ALIGN, "workspace", lambda: _attend(table=(3, 400), max_len=6000, work=BASE + (9 << 20) + 8)),
+    (L.TC_E_ALIGN, "workspace", lambda: _attend(table=(3, 400), max_len=6000, work=BASE + (256 << 20) + 8)),
     (L.TC_E_ALIAS, "input", lambda: _attend(out=BASE + (4 << 20))),
     (L.TC_E_ALIAS, "cache", lambda: _attend(out=BASE + (1 << 20))),
     (L.TC_E_ALIAS, "overlap", lambda: _attend(w=BASE + (24 << 20), wo=BASE + (24 << 20) + 4)),
