@@ -7,11 +7,13 @@ namespace dev {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendRounds = 1;     // rows a lane moves
+constexpr int kAppendStarts = 2048;  // token_starts kept in LDS
 
 // Eight 2-byte values at p: one 16-byte load, or element loads where rows are not 16-byte aligned.
 template <bool WIDE>
 __device__ __forceinline__ u32x4 load8(const unsigned char* p) {
-  if constexpr (WIDE) return *reinterpret_cast<const u32x4*>(p);
+  if constexpr (WIDE) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
   const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
   u32x4 v;
 #pragma unroll
@@ -36,109 +38,137 @@ __device__ __forceinline__ void to_f32(const u32x4& v, float* x) {
 // One row of new values into the pool: `v` are the lane's eight values at element 8 * c of the row
 // (active lanes), `dst` the row, `scale` its scale.  A row's lanes are LPR neighbours.
 //
-// 8-bit rows: scale = amax / 448 and code = x / scale, both divisions correctly rounded, so that the
-// codes are those of the definition evaluated in fp32; e4m3 rounds to nearest even, and amax / scale
-// stays under 448 * (1 + 2^-22), which still rounds to 448.
+// 8-bit rows: scale = amax / 448 and code = x / scale, both quotients correctly rounded, so that the codes are
+// those of the definition evaluated in fp32; e4m3 rounds to nearest even, and amax / scale stays under
+// 448 * (1 + 2^-22), which still rounds to 448.  The magnitudes are compared as integers, where a NaN is above
+// infinity.  The row's quotients share their divisor: with r the rounded reciprocal of scale and q = x r, the
+// remainder x - q scale (exact in one fused step) gives the correctly rounded q + r (x - q scale) (Markstein
+// 1990), 6 operations instead of the division's 11; tiny scales are first multiplied by 2^64 with their x, which
+// keeps the remainder exact, and under an infinite scale the quotients are x r.
 template <bool BF16, bool E4M3, int LPR>
 __device__ __forceinline__ void store_row(const u32x4& v, int c, bool active, unsigned char* dst, float* scale) {
   if constexpr (!E4M3) {
-    if (active) *reinterpret_cast<u32x4*>(dst + 16 * c) = v;
+    if (active) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst + 16 * c));
   } else {
-    float x[8], m = 0.0f;
+    float x[8];
     to_f32<BF16>(v, x);
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = __builtin_fabsf(x[i]);
-      m = m < a || a != a ? a : m;  // a NaN stays: nothing compares with it
+      const uint32_t a = __builtin_bit_cast(uint32_t, x[i]) & 0x7fffffffu;
+      m = m < a ? a : m;
     }
-    if (!active) m = 0.0f;
-#pragma unroll
-    for (int d = 1; d < LPR; d *= 2) {
-      const float o = __shfl_xor(m, d, 64);
-      m = m < o || o != o ? o : m;
-    }
-    float s = m / 448.0f;
+    m = group_max<LPR>(active ? m : 0u);
+    float s = __builtin_bit_cast(float, m) / 448.0f;
     if (s < 1.17549435e-38f) s = 1.0f;
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.0f, d = s * up, r = 1.0f / d;
+    const bool infinite = __builtin_isinf(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = x[i] * up, q = y * r, rest = infinite ? 0.0f : __builtin_fmaf(-q, d, y);
+      x[i] = rest == 0.0f ? q : __builtin_fmaf(rest, r, q);  // (an exact quotient keeps its zero's sign)
+    }
     int w0 = 0, w1 = 0;
-    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] / s, x[1] / s, w0, false);
-    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] / s, x[3] / s, w0, true);
-    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] / s, x[5] / s, w1, false);
-    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] / s, x[7] / s, w1, true);
+    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], w0, false);
+    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w0, true);
+    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], w1, false);
+    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], w1, true);
     if (active) {
-      *reinterpret_cast<u32x2*>(dst + 8 * c) = u32x2{uint32_t(w0), uint32_t(w1)};
+      __builtin_nontemporal_store(u32x2{uint32_t(w0), uint32_t(w1)}, reinterpret_cast<u32x2*>(dst + 8 * c));
       if (c == 0) *scale = s;
     }
   }
 }
 
-// Lanes: LPR a (token, head) row, of which head_dim / 8 move eight values each of the key and of the value.
-// Every lane stays to the end: the row maximum and the search below are exchanges between lanes.
-// Bound: HBM for prompts, the latency of length -> table -> row for single tokens.
+// A workgroup moves kAppendThreads / LPR * kAppendRounds (token, head) rows; LPR lanes a row, of which head_dim / 8
+// move eight values each of the key and of the value.  The rows are on their way while the place of each of the
+// workgroup's tokens is found, once for all its heads: its sequence by a binary search of token_starts (in LDS
+// where they fit), then length, page, offset.
+// Bound: HBM for prompts, the latency of starts -> length -> table -> row for single tokens.
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
 __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs a, Div32 heads) {
-  constexpr int RPW = 64 / LPR;  // rows a wave
-  const int lane = threadIdx.x & 63, c = lane % LPR;
-  const uint32_t row = (blockIdx.x * (kAppendThreads / 64) + threadIdx.x / 64) * RPW + lane / LPR;
-  const uint32_t t = udiv(row, heads);  // rows count heads within tokens; the host keeps them under 2^31
-  const int h = int(row - t * heads.d);
-  const bool mine = t < uint32_t(a.tokens);
-  const bool active = mine && 8 * c < a.head_dim;
-  u32x4 k = {}, v = {};
-  if (active) {
-    k = load8<WIDE>(a.k + int64_t(t) * a.kt + h * a.kh + 16 * c);
-    v = load8<WIDE>(a.v + int64_t(t) * a.vt + h * a.vh + 16 * c);
-  }
-  int b = int(t), pos = -1;
-  if (!a.starts) {
-    if (mine) pos = a.lens[b] - 1;
-  } else {
-    // b = how many of starts[1 .. batch] are <= t, counted 64 at a time by the wave for each of its tokens
-    b = 0;
-    for (int base = 0; base < a.table.batch; base += 64) {
-      const int s = base + lane < a.table.batch ? a.starts[base + lane + 1] : 0x7fffffff;
-      int last = 0;
+  constexpr int RPR = kAppendThreads / LPR;         // rows a round
+  constexpr int ROWS = RPR * kAppendRounds;
+  __shared__ int starts[kAppendStarts];
+  __shared__ int place_seq[ROWS], place_page[ROWS], place_pos[ROWS];  // page -1: nowhere
+  const int tid = threadIdx.x, c = tid % LPR;
+  const uint32_t row0 = blockIdx.x * ROWS, t0 = udiv(row0, heads);  // rows count heads within tokens
+  u32x4 k[kAppendRounds], v[kAppendRounds];
+  uint32_t token[kAppendRounds];
+  int head[kAppendRounds];
 #pragma unroll
-      for (int r = 0; r < RPW; ++r) {
-        const int tr = __builtin_amdgcn_readlane(int(mine ? t : a.tokens - 1), r * LPR);
-        const int n = __popcll(__ballot(s <= tr));
-        if (lane / LPR == r) b += n;
-        last = n;
-      }
-      if (last < 64) break;  // the wave's last token lies before a later sequence
-    }
-    if (mine && b < a.table.batch) {
-      const int first = a.starts[b], end = a.starts[b + 1];
-      if (first <= int(t) && int(t) < end) pos = a.lens[b] - (end - int(t));
+  for (int i = 0; i < kAppendRounds; ++i) {
+    const uint32_t row = row0 + i * RPR + tid / LPR;
+    token[i] = udiv(row, heads);
+    head[i] = int(row - token[i] * heads.d);
+    k[i] = v[i] = u32x4{};
+    if (token[i] < uint32_t(a.tokens) && 8 * c < a.head_dim) {
+      k[i] = load8<WIDE>(a.k + int64_t(token[i]) * a.kt + head[i] * a.kh + 16 * c);
+      v[i] = load8<WIDE>(a.v + int64_t(token[i]) * a.vt + head[i] * a.vh + 16 * c);
     }
   }
-  int page = -1;
-  uint32_t r = 0;
-  if (pos >= 0) {
-    const uint32_t col = udiv(uint32_t(pos), a.pool.div);
-    r = uint32_t(pos) - col * a.pool.div.d;
-    if (col < uint32_t(a.table.cols)) page = paged_page(a.table, a.pool, b, col);
-  }
-  const bool out = active && page >= 0;
   const PagedPool& p = a.pool;
-  unsigned char* kd = nullptr;
-  unsigned char* vd = nullptr;
-  float *ks = nullptr, *vs = nullptr;
-  if (out) {
-    kd = p.k + page * p.kp + r * p.kr + h * p.kh;
-    vd = p.v + page * p.vp + r * p.vr + h * p.vh;
-    if constexpr (E4M3) {
-      ks = p.ks + page * p.ksp + r * p.ksr + h * p.ksh;
-      vs = p.vs + page * p.vsp + r * p.vsr + h * p.vsh;
-    }
-    if (a.weights && c == 0 && pos < a.w.cols) a.weights[b * a.w.sb + h * a.w.sh + pos * a.w.sc] = 0.0f;
+  const int batch = a.table.batch;
+  const bool listed = a.starts && batch < kAppendStarts;
+  if (listed) {
+    for (int i = tid; i <= batch; i += kAppendThreads) starts[i] = a.starts[i];
+    __syncthreads();
   }
-  store_row<BF16, E4M3, LPR>(k, c, out, kd, ks);
-  store_row<BF16, E4M3, LPR>(v, c, out, vd, vs);
+  // the workgroup's tokens, at most ROWS (one head) of them
+  static_assert(ROWS <= kAppendThreads);
+  if (tid < ROWS) {
+    const uint32_t t = t0 + tid;
+    int b = int(t), pos = -1, page = -1;
+    if (t < uint32_t(a.tokens) && t <= udiv(row0 + ROWS - 1, heads)) {
+      if (!a.starts) {
+        pos = a.lens[b] - 1;
+      } else {
+        // the last b with starts[b] <= t
+        int lo = 0, hi = batch;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if ((listed ? starts[mid] : a.starts[mid]) <= int(t)) lo = mid; else hi = mid;
+        }
+        b = lo;
+        const int first = listed ? starts[b] : a.starts[b], end = listed ? starts[b + 1] : a.starts[b + 1];
+        if (first <= int(t) && int(t) < end) pos = a.lens[b] - (end - int(t));
+      }
+      if (pos >= 0) {
+        const uint32_t col = udiv(uint32_t(pos), p.div);
+        if (col < uint32_t(a.table.cols)) page = paged_page(a.table, p, b, col);
+      }
+    }
+    place_seq[tid] = b;
+    place_page[tid] = page;
+    place_pos[tid] = pos;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAppendRounds; ++i) {
+    const int at = int(token[i] - t0), b = place_seq[at], page = place_page[at], pos = place_pos[at];
+    const bool out = page >= 0 && 8 * c < a.head_dim;
+    const int h = head[i];
+    unsigned char* kd = nullptr;
+    unsigned char* vd = nullptr;
+    float *ks = nullptr, *vs = nullptr;
+    if (out) {
+      const uint32_t r = uint32_t(pos) - udiv(uint32_t(pos), p.div) * p.div.d;
+      kd = p.k + page * p.kp + r * p.kr + h * p.kh;
+      vd = p.v + page * p.vp + r * p.vr + h * p.vh;
+      if constexpr (E4M3) {
+        ks = p.ks + page * p.ksp + r * p.ksr + h * p.ksh;
+        vs = p.vs + page * p.vsp + r * p.vsr + h * p.vsh;
+      }
+      if (a.weights && c == 0 && pos < a.w.cols) a.weights[b * a.w.sb + h * a.w.sh + pos * a.w.sc] = 0.0f;
+    }
+    store_row<BF16, E4M3, LPR>(k[i], c, out, kd, ks);
+    store_row<BF16, E4M3, LPR>(v[i], c, out, vd, vs);
+  }
 }
 
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
 void launch(const AppendArgs& a, hipStream_t s) {
-  const int64_t per = kAppendThreads / LPR;
+  const int64_t per = kAppendThreads / LPR * kAppendRounds;
   const int64_t wgs = (a.tokens * a.heads + per - 1) / per;
   hipLaunchKernelGGL((paged_append_kernel<BF16, E4M3, WIDE, LPR>), dim3(uint32_t(wgs)), dim3(kAppendThreads), 0, s, a,
                      make_div32(uint32_t(a.heads)));

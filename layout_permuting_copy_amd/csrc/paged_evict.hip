@@ -4,10 +4,7 @@
 namespace tc {
 namespace dev {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWaves = kSelectThreads / 64;
 constexpr int kBins = 2048;  // histogram bins: 11 bits of a key
-constexpr int kHists = 4;    // copies of the histogram, one for every fourth wave
 
 // An unsigned integer that orders weights as numbers: equal zeros, any NaN above all.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -17,152 +14,204 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The sum of x[0 .. wave - 1] (WAVES <= 16 values in LDS, one a lane).
+template <int WAVES>
+__device__ __forceinline__ uint32_t sum_below(const uint32_t* x, int wave, int lane) {
+  const uint32_t upto = wave_scan(lane < WAVES ? x[lane] : 0u);
+  return wave ? uint32_t(__builtin_amdgcn_readlane(int(upto), wave - 1)) : 0u;
+}
+
 // One workgroup a (sequence, head): the kept rows of a sequence over its budget.  The budget -
-// recent heaviest of the first n - recent rows are those with key > T and the first `need` with
+// recent heaviest of the first n - recent rows are those with key > T and the first `left` with
 // key == T; T is found by a radix selection of 11 + 11 + 10 bits from the top, each pass a
-// histogram in LDS of the keys that share the digits found so far.  Every wave owns a stretch of
-// the rows, so a walk in order needs only the waves' counts to place what it keeps.
-// Bound: the passes over the weights, which after the first come from the caches.
-__global__ __launch_bounds__(kSelectThreads) void paged_select_kernel(EvictArgs a, Div32 heads) {
+// histogram in LDS of the keys that share the digits found so far, ended as soon as every key with
+// those digits stays.  Every wave owns a stretch of the rows, so a walk in order needs only the waves' counts to
+// place what it keeps.
+//
+// KEYS: weights a lane holds in registers (one read of the weights; THREADS * KEYS rows at most), or 0: every
+// pass reads them again, from the caches.  HISTS: copies of the histogram, one for every HISTS-th wave, so that
+// fewer lanes add to one bin.  Bound: barriers and LDS atomics; few (sequence, head) leave most CUs idle.
+template <int THREADS, int KEYS, int HISTS>
+__global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div32 heads) {
+  constexpr int WAVES = THREADS / 64, BPT = kBins / THREADS;  // bins a thread sums
   const int b = int(udiv(blockIdx.x, heads)), h = int(blockIdx.x - uint32_t(b) * heads.d);
   const int n = paged_len(a.lens, b, a.max_len);
   const int kept_n = n < a.budget ? n : a.budget;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int32_t* kept = a.kept + b * a.kr.sb + h * a.kr.sh;
   const float* w = a.weights + b * a.w.sb + h * a.w.sh;
   float* wo = a.weights_out ? a.weights_out + b * a.wo.sb + h * a.wo.sh : nullptr;
   if (h == 0 && tid == 0) a.lens_out[b] = kept_n;
-  for (int64_t j = kept_n + tid; j < a.kr.cols; j += kSelectThreads) kept[j * a.kr.sc] = -1;
+  for (int64_t j = kept_n + tid; j < a.kr.cols; j += THREADS) kept[j * a.kr.sc] = -1;
   if (n <= a.budget) {
-    for (int j = tid; j < n; j += kSelectThreads) {
+    for (int j = tid; j < n; j += THREADS) {
       kept[j * a.kr.sc] = j;
       if (wo) wo[j * a.wo.sc] = w[j * a.w.sc];
     }
     return;
   }
   const int cand = n - a.recent, want = a.budget - a.recent;  // cand > want >= 0
-  for (int j = tid; j < a.recent; j += kSelectThreads) {
+  const int seg = ((cand + WAVES - 1) / WAVES + 63) / 64 * 64;  // at most 64 * KEYS, if those are held
+  const int lo = wave * seg, hi = lo + seg < cand ? lo + seg : cand;
+  float held[KEYS ? KEYS : 1];
+#pragma unroll
+  for (int k = 0; k < KEYS; ++k) held[k] = lo + 64 * k + lane < hi ? w[(lo + 64 * k + lane) * a.w.sc] : 0.0f;
+  for (int j = tid; j < a.recent; j += THREADS) {
     kept[(want + j) * a.kr.sc] = cand + j;
     if (wo) wo[(want + j) * a.wo.sc] = w[(cand + j) * a.w.sc];
   }
   if (want == 0) return;
+  // f(row, weight, whether the lane has one) over the wave's rows, 64 at a time, in order
+  const auto each = [&](auto f) {
+    if constexpr (KEYS > 0) {
+#pragma unroll
+      for (int k = 0; k < KEYS; ++k)
+        if (lo + 64 * k < hi) f(lo + 64 * k + lane, held[k], lo + 64 * k + lane < hi);
+    } else {
+      for (int i = lo + lane; i - lane < hi; i += 64) f(i, i < hi ? w[i * a.w.sc] : 0.0f, i < hi);
+    }
+  };
 
-  __shared__ uint32_t hist[kHists][kBins];
-  __shared__ uint32_t wave_sum[kSelectWaves], wave_eq[kSelectWaves];
-  __shared__ uint32_t found_digit, found_above;
-  const int seg = ((cand + kSelectWaves - 1) / kSelectWaves + 63) / 64 * 64;
-  const int lo = wave * seg, hi = lo + seg < cand ? lo + seg : cand;
-
+  __shared__ uint32_t hist[HISTS][kBins];
+  __shared__ uint32_t wave_sum[WAVES], wave_eq[WAVES];
+  __shared__ uint32_t found_digit, found_above, found_count;
   uint32_t prefix = 0, mask = 0;
-  int left = want;  // keys still to be found among those that match the prefix
+  uint32_t left = uint32_t(want);  // keys still to be found among those that match the prefix
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t bins = pass == 2 ? 1024 : 2048;
-    for (int i = tid; i < kHists * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < HISTS * kBins / 4; i += THREADS) reinterpret_cast<u32x4*>(&hist[0][0])[i] = u32x4{};
     __syncthreads();
-    for (int i = lo + lane; i < hi; i += 64) {
-      const uint32_t key = weight_key(w[i * a.w.sc]);
-      if ((key & mask) == prefix) atomicAdd(&hist[wave % kHists][(key >> shift) & (bins - 1)], 1u);
-    }
+    each([&](int, float x, bool in) {
+      const uint32_t key = weight_key(x);
+      if (in && (key & mask) == prefix) atomicAdd(&hist[wave % HISTS][(key >> shift) & (bins - 1)], 1u);
+    });
     __syncthreads();
-    // bins from the top: thread t holds bins 2047 - 2 t and 2046 - 2 t; the wanted bin is where
-    // the running count from the top first reaches `left`
-    const int top = kBins - 1 - 2 * tid;
-    uint32_t c0 = 0, c1 = 0;
+    // thread t sums the BPT bins below kBins - BPT * t; the wanted bin is where the count from the top first
+    // reaches `left`
+    const int top = kBins - 1 - BPT * tid;
+    uint32_t c[BPT], sum = 0;
 #pragma unroll
-    for (int k = 0; k < kHists; ++k) {
-      c0 += hist[k][top];
-      c1 += hist[k][top - 1];
-    }
-    uint32_t sum = c0 + c1;
+    for (int k = 0; k < BPT; ++k) {
+      c[k] = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const uint32_t o = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += o;
+      for (int i = 0; i < HISTS; ++i) c[k] += hist[i][top - k];
+      sum += c[k];
     }
-    if (lane == 63) wave_sum[wave] = sum;
+    const uint32_t upto = wave_scan(sum);
+    if (lane == 63) wave_sum[wave] = upto;
     __syncthreads();
-    uint32_t before = sum - c0 - c1;
-    for (int k = 0; k < wave; ++k) before += wave_sum[k];
-    if (before < uint32_t(left) && before + c0 + c1 >= uint32_t(left)) {
-      const bool first = before + c0 >= uint32_t(left);
-      found_digit = uint32_t(first ? top : top - 1);
-      found_above = first ? before : before + c0;
+    uint32_t before = upto - sum + sum_below<WAVES>(wave_sum, wave, lane);
+    if (before < left && before + sum >= left) {
+#pragma unroll
+      for (int k = 0; k < BPT; ++k) {
+        if (before < left && before + c[k] >= left) {
+          found_digit = uint32_t(top - k);
+          found_above = before;
+          found_count = c[k];
+        }
+        before += c[k];
+      }
     }
     __syncthreads();
     prefix |= found_digit << shift;
     mask |= (bins - 1) << shift;
-    left -= int(found_above);
+    left -= found_above;
+    if (found_count == left) break;
     __syncthreads();  // found_*, wave_sum and hist are written again
   }
+  __syncthreads();
 
-  // T = prefix; `left` of the keys equal to it stay, the lowest rows first
+  // keys above the prefix stay, and `left` of those equal to it, the lowest rows first
   uint32_t gt = 0, eq = 0;
-  for (int i = lo + lane; i - lane < hi; i += 64) {
-    const uint32_t key = i < hi ? weight_key(w[i * a.w.sc]) : 0;
-    gt += __popcll(__ballot(i < hi && key > prefix));
-    eq += __popcll(__ballot(i < hi && key == prefix));
-  }
+  each([&](int, float x, bool in) {
+    const uint32_t key = weight_key(x) & mask;
+    gt += __popcll(__ballot(in && key > prefix));
+    eq += __popcll(__ballot(in && key == prefix));
+  });
   if (lane == 0) {
     wave_sum[wave] = gt;
     wave_eq[wave] = eq;
   }
   __syncthreads();
-  uint32_t gt_before = 0, eq_before = 0;
-  for (int k = 0; k < wave; ++k) {
-    gt_before += wave_sum[k];
-    eq_before += wave_eq[k];
-  }
+  uint32_t gt_before = sum_below<WAVES>(wave_sum, wave, lane), eq_before = sum_below<WAVES>(wave_eq, wave, lane);
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  for (int i = lo + lane; i - lane < hi; i += 64) {
-    const float x = i < hi ? w[i * a.w.sc] : 0.0f;
-    const uint32_t key = weight_key(x);
-    const uint64_t g = __ballot(i < hi && key > prefix), e = __ballot(i < hi && key == prefix);
+  each([&](int i, float x, bool in) {
+    const uint32_t key = weight_key(x) & mask;
+    const uint64_t g = __ballot(in && key > prefix), e = __ballot(in && key == prefix);
     const uint32_t eq_rank = eq_before + __popcll(e & below);
-    const uint32_t ties = eq_rank < uint32_t(left) ? eq_rank : uint32_t(left);  // kept ties below this row
-    const bool keep = (g >> lane & 1) || ((e >> lane & 1) && eq_rank < uint32_t(left));
-    if (keep) {
+    const uint32_t ties = eq_rank < left ? eq_rank : left;  // kept ties below this row
+    if ((g >> lane & 1) || ((e >> lane & 1) && eq_rank < left)) {
       const int64_t j = gt_before + __popcll(g & below) + ties;
       kept[j * a.kr.sc] = i;
       if (wo) wo[j * a.wo.sc] = x;
     }
     gt_before += __popcll(g);
     eq_before += __popcll(e);
-  }
+  });
+}
+
+template <int THREADS, int KEYS, int HISTS>
+void select(const EvictArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((paged_select_kernel<THREADS, KEYS, HISTS>), dim3(uint32_t(a.table.batch * a.heads)), dim3(THREADS), 0, s, a,
+                     make_div32(uint32_t(a.heads)));
 }
 
 constexpr int kCopyThreads = 256;
+constexpr int kCopyRounds = 1;  // rows a lane moves
 
-// The kept rows of keys and values into their new pages: LPR lanes a row, 16 bytes a lane.
-// Grid: (sequence, head) times `chunks` workgroups over the rows.  Bound: HBM.
+// The kept rows of keys and values into their new pages: LPR lanes a row, 16 bytes a lane, kCopyRounds rows
+// on their way at once.  Grid: (sequence, rows, head), the heads fastest: those of the same new rows are neighbours
+// where a pool keeps a row's heads together.  Bound: HBM.
 template <bool E4M3, int LPR>
 __global__ __launch_bounds__(kCopyThreads) void paged_move_kernel(EvictArgs a, Div32 heads, Div32 chunks) {
-  constexpr int RPW = kCopyThreads / LPR;
-  const uint32_t bh = udiv(blockIdx.x, chunks), chunk = blockIdx.x - bh * chunks.d;
-  const int b = int(udiv(bh, heads)), h = int(bh - uint32_t(b) * heads.d);
+  constexpr int RPR = kCopyThreads / LPR;
+  const uint32_t bc = udiv(blockIdx.x, heads), bb = udiv(bc, chunks), chunk = bc - bb * chunks.d;
+  const int b = int(bb), h = int(blockIdx.x - bc * heads.d);
   const int n = paged_len(a.lens, b, a.max_len);
   const int kept_n = n < a.budget ? n : a.budget;
-  const int j = int(chunk) * RPW + int(threadIdx.x) / LPR, c = threadIdx.x % LPR;
-  if (j >= kept_n || 16 * c >= a.row_bytes) return;
-  const int i = a.kept[b * a.kr.sb + h * a.kr.sh + j * a.kr.sc];
-  const uint32_t sc = udiv(uint32_t(i), a.src.div), dc = udiv(uint32_t(j), a.dst.div);
-  const uint32_t sr = uint32_t(i) - sc * a.src.div.d, dr = uint32_t(j) - dc * a.dst.div.d;
-  const int sp = paged_page(a.table, a.src, b, sc), dp = paged_page(a.dst_table, a.dst, b, dc);
-  if (sp < 0 || dp < 0) return;
-  const u32x4 k = *reinterpret_cast<const u32x4*>(a.src.k + sp * a.src.kp + sr * a.src.kr + h * a.src.kh + 16 * c);
-  const u32x4 v = *reinterpret_cast<const u32x4*>(a.src.v + sp * a.src.vp + sr * a.src.vr + h * a.src.vh + 16 * c);
-  *reinterpret_cast<u32x4*>(a.dst.k + dp * a.dst.kp + dr * a.dst.kr + h * a.dst.kh + 16 * c) = k;
-  *reinterpret_cast<u32x4*>(a.dst.v + dp * a.dst.vp + dr * a.dst.vr + h * a.dst.vh + 16 * c) = v;
-  if (E4M3 && c == 0) {
-    a.dst.ks[dp * a.dst.ksp + dr * a.dst.ksr + h * a.dst.ksh] = a.src.ks[sp * a.src.ksp + sr * a.src.ksr + h * a.src.ksh];
-    a.dst.vs[dp * a.dst.vsp + dr * a.dst.vsr + h * a.dst.vsh] = a.src.vs[sp * a.src.vsp + sr * a.src.vsr + h * a.src.vsh];
+  const int j0 = int(chunk) * RPR * kCopyRounds + int(threadIdx.x) / LPR, c = threadIdx.x % LPR;
+  if (int(chunk) * RPR * kCopyRounds >= kept_n) return;
+  const int32_t* kept = a.kept + b * a.kr.sb + h * a.kr.sh;
+  int from[kCopyRounds], sp[kCopyRounds], dp[kCopyRounds];
+#pragma unroll
+  for (int r = 0; r < kCopyRounds; ++r) {
+    const int j = j0 + r * RPR;
+    from[r] = kept[(j < kept_n ? j : 0) * a.kr.sc];
+    dp[r] = j < kept_n ? paged_page(a.dst_table, a.dst, b, udiv(uint32_t(j), a.dst.div)) : -1;
+  }
+  u32x4 k[kCopyRounds], v[kCopyRounds];
+  float ks[kCopyRounds], vs[kCopyRounds];
+#pragma unroll
+  for (int r = 0; r < kCopyRounds; ++r) sp[r] = paged_page(a.table, a.src, b, udiv(uint32_t(from[r]), a.src.div));
+#pragma unroll
+  for (int r = 0; r < kCopyRounds; ++r) {
+    if (sp[r] < 0 || dp[r] < 0 || 16 * c >= a.row_bytes) continue;
+    const uint32_t row = uint32_t(from[r]) - udiv(uint32_t(from[r]), a.src.div) * a.src.div.d;
+    gload<16, 1>(a.src.k + sp[r] * a.src.kp + row * a.src.kr + h * a.src.kh + 16 * c, reinterpret_cast<uint32_t*>(&k[r]));
+    gload<16, 1>(a.src.v + sp[r] * a.src.vp + row * a.src.vr + h * a.src.vh + 16 * c, reinterpret_cast<uint32_t*>(&v[r]));
+    if (E4M3 && c == 0) {
+      ks[r] = a.src.ks[sp[r] * a.src.ksp + row * a.src.ksr + h * a.src.ksh];
+      vs[r] = a.src.vs[sp[r] * a.src.vsp + row * a.src.vsr + h * a.src.vsh];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kCopyRounds; ++r) {
+    if (sp[r] < 0 || dp[r] < 0 || 16 * c >= a.row_bytes) continue;
+    const uint32_t j = uint32_t(j0 + r * RPR), row = j - udiv(j, a.dst.div) * a.dst.div.d;
+    gstore<16, 2>(a.dst.k + dp[r] * a.dst.kp + row * a.dst.kr + h * a.dst.kh + 16 * c, reinterpret_cast<uint32_t*>(&k[r]));
+    gstore<16, 2>(a.dst.v + dp[r] * a.dst.vp + row * a.dst.vr + h * a.dst.vh + 16 * c, reinterpret_cast<uint32_t*>(&v[r]));
+    if (E4M3 && c == 0) {
+      a.dst.ks[dp[r] * a.dst.ksp + row * a.dst.ksr + h * a.dst.ksh] = ks[r];
+      a.dst.vs[dp[r] * a.dst.vsp + row * a.dst.vsr + h * a.dst.vsh] = vs[r];
+    }
   }
 }
 
 template <bool E4M3, int LPR>
 int move(const EvictArgs& a, int most, hipStream_t s) {
-  constexpr int per = kCopyThreads / LPR;
+  constexpr int per = kCopyThreads / LPR * kCopyRounds;
   const int64_t chunks = (int64_t(most) + per - 1) / per, wgs = chunks * a.table.batch * a.heads;
   if (wgs >= int64_t(1) << 31) return TC_E_RANGE;
   hipLaunchKernelGGL((paged_move_kernel<E4M3, LPR>), dim3(uint32_t(wgs)), dim3(kCopyThreads), 0, s, a,
@@ -188,8 +237,16 @@ int launch_paged_evict(const EvictArgs& a, int cache_dtype, void* stream) {
   const int most = a.budget < a.max_len ? a.budget : a.max_len;
   // the move's grid has to fit before anything is launched (8 rows a workgroup at the widest rows)
   if ((int64_t(most) / 8 + 1) * a.table.batch * a.heads >= int64_t(1) << 31) return TC_E_RANGE;
-  hipLaunchKernelGGL(dev::paged_select_kernel, dim3(uint32_t(a.table.batch * a.heads)), dim3(dev::kSelectThreads), 0, s, a,
-                     make_div32(uint32_t(a.heads)));
+  if (a.max_len <= 1024)
+    dev::select<256, 4, 1>(a, s);
+  else if (a.max_len <= 4096)
+    dev::select<1024, 4, 2>(a, s);
+  else if (a.max_len <= 16384)
+    dev::select<1024, 16, 4>(a, s);
+  else if (a.max_len <= 32768)
+    dev::select<1024, 32, 4>(a, s);
+  else
+    dev::select<1024, 0, 4>(a, s);
   if (most == 0) return TC_OK;
   return cache_dtype == TC_E4M3 ? dev::move_rows<true>(a, most, s) : dev::move_rows<false>(a, most, s);
 }
