@@ -376,7 +376,7 @@ class PagedCache:
     bfloat16, or float8_e4m3fn with float32 ``k_scale`` and ``v_scale`` of shape (pages, page_size, heads).
     Holds the tensors; the layouts are read from them once."""
 
-    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_c", "_ref", "device")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_c", "_ref", "device", "pages", "page_size", "heads", "head_dim")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _import_torch()
@@ -396,6 +396,10 @@ class PagedCache:
                 setattr(c, name, x.data_ptr())
                 setattr(c, name + "_layout", make_layout(x.shape, x.stride()))
         _device_of(self, v, k_scale, v_scale)
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError(f"keys and values must have one shape (pages, page_size, heads, head_dim), got {tuple(k.shape)} "
+                             f"and {tuple(v.shape)}")
+        self.pages, self.page_size, self.heads, self.head_dim = k.shape
         self._c = c
         self._ref = ctypes.addressof(c)
 
@@ -403,22 +407,22 @@ class PagedCache:
     v = property(lambda self: self._v)
     k_scale = property(lambda self: self._k_scale)
     v_scale = property(lambda self: self._v_scale)
-    pages = property(lambda self: self._k.shape[0])
-    page_size = property(lambda self: self._k.shape[1])
-    heads = property(lambda self: self._k.shape[2])
-    head_dim = property(lambda self: self._k.shape[3])
 
 
-_torch = None
+_torch = _here = _raw_stream = None
 _T_I32 = _T_F32 = None
 _PAGED_DTYPES = {}
 
 
 def _import_torch():
     """torch and the types the paged entry points name, looked up once."""
-    global _torch, _T_I32, _T_F32
+    global _torch, _T_I32, _T_F32, _here, _raw_stream
     if _torch is None:
         import torch
+        # the current device and stream without the public calls' wrappers (0.1 us each; current_stream() takes 2.5)
+        _here = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda index: torch.cuda.current_stream(index).cuda_stream))
         _T_I32, _T_F32 = torch.int32, torch.float32
         _PAGED_DTYPES.update({torch.float16: TC_F16, torch.bfloat16: TC_BF16, torch.float8_e4m3fn: TC_E4M3})
         _torch = torch
@@ -446,9 +450,8 @@ def _device_of(cache, *tensors):
 
 
 def _vector(name: str, x, n: int) -> int:
-    _want(name, x, _T_I32)
-    if x.shape != (n,) or (n > 1 and x.stride() != (1,)):
-        raise ValueError(f"{name} must be contiguous with {n} elements")
+    if x.dtype != _T_I32 or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} must be int32, contiguous, with {n} elements, got {x.dtype} {tuple(x.shape)}")
     return x.data_ptr()
 
 
@@ -472,28 +475,33 @@ def _enter(dev):
     """Makes the tensors' device current; returns the one to go back to, or None."""
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not {dev}")
-    here = _torch.cuda.current_device()
+    here = _here()
     if here == dev.index:
         return None
     _torch.cuda.set_device(dev)
     return here
 
 
-def _paged_stream(dev, stream) -> int:
-    if stream is not None:
-        return _stream(stream)
-    try:
-        return _torch._C._cuda_getCurrentRawStream(dev.index)  # 0.1 us; current_stream() takes 2.5
-    except AttributeError:
-        return _torch.cuda.current_stream().cuda_stream
-
-
-def _empty_on(handle, stream, dev, shape, dtype):
+def _empty_on(handle, dev, shape, dtype):
     """Memory for this call, allocated on its stream: another stream's next use of it waits its turn."""
-    if stream is None or handle == _torch.cuda.current_stream().cuda_stream:
+    if handle == _raw_stream(dev.index):
         return _torch.empty(shape, dtype=dtype, device=dev)
     with _torch.cuda.stream(_torch.cuda.ExternalStream(handle, device=dev)):
         return _torch.empty(shape, dtype=dtype, device=dev)
+
+
+_workspace_cache = {}
+
+
+def _workspace(lib, key) -> int:
+    """tc_paged_attention_workspace of these sizes."""
+    need = lib.tc_paged_attention_workspace(*key)
+    if need < 0:
+        _check(need)
+    if len(_workspace_cache) >= 4096:
+        _workspace_cache.clear()
+    _workspace_cache[key] = need
+    return need
 
 
 def tc_paged_append(cache: PagedCache, k, v, block_table, seq_lens, token_starts=None, weights=None,
@@ -506,7 +514,11 @@ def tc_paged_append(cache: PagedCache, k, v, block_table, seq_lens, token_starts
     tokens starts[b] .. starts[b + 1] - 1 become its last rows and tokens past starts[batch] are padding.
     ``weights`` (batch, heads, capacity) float32, if given, is zeroed for the new rows."""
     lib = _lib or load_library()
-    dev = _device_of(cache, k, v, block_table, seq_lens, token_starts, weights)
+    dev = cache.device
+    if k.device != dev or v.device != dev or block_table.device != dev or seq_lens.device != dev:
+        _device_of(cache, k, v, block_table, seq_lens)
+    if token_starts is not None or weights is not None:
+        _device_of(cache, token_starts, weights)
     if k.dtype != v.dtype:
         raise ValueError(f"keys are {k.dtype}, values {v.dtype}")
     _want("block_table", block_table, _T_I32)
@@ -521,7 +533,8 @@ def tc_paged_append(cache: PagedCache, k, v, block_table, seq_lens, token_starts
     back = _enter(dev)
     try:
         rc = lib.tc_paged_append(cache._ref, k.data_ptr(), kl[0], v.data_ptr(), vl[0], _paged_dtype(k),
-                                 block_table.data_ptr(), tl[0], lens, starts, wp, wl[0], _paged_stream(dev, stream))
+                                 block_table.data_ptr(), tl[0], lens, starts, wp, wl[0],
+                                 _raw_stream(dev.index) if stream is None else _stream(stream))
     finally:
         if back is not None:
             _torch.cuda.set_device(back)
@@ -539,7 +552,11 @@ def tc_paged_attention(q, cache: PagedCache, block_table, seq_lens, scale: Optio
     sums.  ``weights`` (batch, heads, capacity) float32: ``weights_out`` (default: ``weights`` itself) receives
     weights plus each row's attention weight summed over the query heads of its cache head."""
     lib = _lib or load_library()
-    dev = _device_of(cache, q, block_table, seq_lens, out, lse, weights, weights_out)
+    dev = cache.device
+    if q.device != dev or block_table.device != dev or seq_lens.device != dev:
+        _device_of(cache, q, block_table, seq_lens)
+    if out is not None or lse is not None or weights is not None:
+        _device_of(cache, out, lse, weights, weights_out)
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be (batch, q_heads, head_dim), block_table (batch, columns)")
     _want("block_table", block_table, _T_I32)
@@ -566,16 +583,17 @@ def tc_paged_attention(q, cache: PagedCache, block_table, seq_lens, scale: Optio
     ql, tl = _lay(q), _lay(block_table)
     back = _enter(dev)
     try:
-        handle = _paged_stream(dev, stream)
+        handle = _raw_stream(dev.index) if stream is None else _stream(stream)
         if out is None:
-            out = _empty_on(handle, stream, dev, q.shape, q.dtype)
+            out = _torch.empty_like(q) if stream is None else _empty_on(handle, dev, q.shape, q.dtype)
         elif out.dtype != q.dtype:
             raise ValueError(f"out is {out.dtype}, q {q.dtype}")
         ol = _lay(out)
-        need = lib.tc_paged_attention_workspace(batch, q_heads, cache.heads, dim, max_len, weights is not None)
-        if need < 0:
-            _check(need)
-        work = _empty_on(handle, stream, dev, need, _torch.uint8) if need else None
+        key = (batch, q_heads, cache.heads, dim, max_len, weights is not None)
+        need = _workspace_cache.get(key)
+        if need is None:
+            need = _workspace(lib, key)
+        work = _empty_on(handle, dev, need, _torch.uint8) if need else None
         rc = lib.tc_paged_attention(cache._ref, q.data_ptr(), ql[0], out.data_ptr(), ol[0], code, block_table.data_ptr(), tl[0],
                                     lens, max_len, scale, lp, ll[0], wp, wl[0], wop, wol[0],
                                     None if work is None else work.data_ptr(), need, handle)
@@ -613,11 +631,11 @@ def tc_paged_evict(src: PagedCache, block_table, seq_lens, weights, dst: PagedCa
     tl, wl, dl = _lay(block_table), _lay(weights), _lay(dst_table)
     back = _enter(dev)
     try:
-        handle = _paged_stream(dev, stream)
+        handle = _raw_stream(dev.index) if stream is None else _stream(stream)
         if lens_out is None:
-            lens_out = _empty_on(handle, stream, dev, batch, _T_I32)
+            lens_out = _empty_on(handle, dev, batch, _T_I32)
         if kept is None:
-            kept = _empty_on(handle, stream, dev, (batch, src.heads, max(0, min(budget, max_len))), _T_I32)
+            kept = _empty_on(handle, dev, (batch, src.heads, max(0, min(budget, max_len))), _T_I32)
         _want("kept", kept, _T_I32)
         kl = _lay(kept)
         rc = lib.tc_paged_evict(src._ref, block_table.data_ptr(), tl[0], lens, max_len, weights.data_ptr(), wl[0],

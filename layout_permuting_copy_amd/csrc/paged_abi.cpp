@@ -41,28 +41,29 @@ struct Operand {
   bool empty;
 };
 
+[[noreturn]] void refuse_operand(int code, const char* name, const char* why) { refuse(code, std::string(name) + why); }
+
 Operand operand(const char* name, const void* p, const tc_layout* l, int rank, int eb) {
-  const std::string n(name);
-  need(l != nullptr, TC_E_NULL, (n + ": null layout").c_str());
-  if (l->rank != rank) refuse(TC_E_RANK, n + ": expected " + std::to_string(rank) + " modes");
+  if (!l) refuse_operand(TC_E_NULL, name, ": null layout");
+  if (l->rank != rank) refuse(TC_E_RANK, std::string(name) + ": expected " + std::to_string(rank) + " modes");
   Operand o{};
   o.empty = false;
   __int128 hi = 0;
-  need(l->offset >= -kLim && l->offset <= kLim, TC_E_RANGE, (n + ": offset beyond 2^58").c_str());
+  if (l->offset < -kLim || l->offset > kLim) refuse_operand(TC_E_RANGE, name, ": offset beyond 2^58");
   for (int k = 0; k < rank; ++k) {
-    if (l->shape[k] < 0) refuse(TC_E_EXTENT, n + ": negative extent");
+    if (l->shape[k] < 0) refuse_operand(TC_E_EXTENT, name, ": negative extent");
     o.e[k] = l->shape[k];
     o.empty = o.empty || o.e[k] == 0;
     if (o.e[k] > 1) {
-      if (l->stride[k] < 0) refuse(TC_E_ARG, n + ": negative stride");
+      if (l->stride[k] < 0) refuse_operand(TC_E_ARG, name, ": negative stride");
       hi += __int128(o.e[k] - 1) * l->stride[k];
-      if (l->stride[k] > kLim || hi > kLim) refuse(TC_E_RANGE, n + ": element offsets beyond 2^58");
+      if (l->stride[k] > kLim || hi > kLim) refuse_operand(TC_E_RANGE, name, ": element offsets beyond 2^58");
       o.s[k] = l->stride[k] * eb;
     }
   }
   if (o.empty) return o;
-  need(p != nullptr, TC_E_NULL, (n + ": null pointer").c_str());
-  if (reinterpret_cast<uintptr_t>(p) % uintptr_t(eb)) refuse(TC_E_ALIGN, n + ": pointer not aligned to its elements");
+  if (!p) refuse_operand(TC_E_NULL, name, ": null pointer");
+  if (reinterpret_cast<uintptr_t>(p) % uintptr_t(eb)) refuse_operand(TC_E_ALIGN, name, ": pointer not aligned to its elements");
   const __int128 base = __int128(reinterpret_cast<uintptr_t>(p)) + __int128(l->offset) * eb;
   o.p = reinterpret_cast<unsigned char*>(uintptr_t(base));
   o.r = Range{base, base + hi * eb + eb};
@@ -136,15 +137,15 @@ struct Pool {
 };
 
 Pool pool_of(const char* name, const tc_paged_cache* c, bool written) {
-  const std::string n(name);
-  need(c != nullptr, TC_E_NULL, (n + ": null cache").c_str());
+  const std::string n(name);  // (short enough to need no allocation)
+  if (!c) refuse(TC_E_NULL, n + ": null cache");
   Pool o{};
   o.dtype = c->dtype;
   o.eb = c->dtype == TC_E4M3 ? 1 : (c->dtype == TC_F16 || c->dtype == TC_BF16) ? 2 : 0;
   if (!o.eb) refuse(TC_E_DTYPE, n + ": dtype must be TC_F16, TC_BF16 or TC_E4M3");
   const bool quantised = c->dtype == TC_E4M3;
-  o.k = operand((n + ".k").c_str(), c->k, &c->k_layout, 4, o.eb);
-  o.v = operand((n + ".v").c_str(), c->v, &c->v_layout, 4, o.eb);
+  o.k = operand("keys", c->k, &c->k_layout, 4, o.eb);
+  o.v = operand("values", c->v, &c->v_layout, 4, o.eb);
   for (int i = 0; i < 4; ++i)
     if (o.k.e[i] != o.v.e[i]) refuse(TC_E_EXTENT, n + ": keys and values differ in shape");
   o.pages = o.k.e[0];
@@ -159,8 +160,8 @@ Pool pool_of(const char* name, const tc_paged_cache* c, bool written) {
     refuse(TC_E_RANGE, n + ": pages, page_size and heads must fit 31 bits");
   o.empty = o.k.empty;
   if (quantised) {
-    o.ks = operand((n + ".k_scale").c_str(), c->k_scale, &c->k_scale_layout, 3, 4);
-    o.vs = operand((n + ".v_scale").c_str(), c->v_scale, &c->v_scale_layout, 3, 4);
+    o.ks = operand("k_scale", c->k_scale, &c->k_scale_layout, 3, 4);
+    o.vs = operand("v_scale", c->v_scale, &c->v_scale_layout, 3, 4);
     for (int i = 0; i < 3; ++i)
       if (o.ks.e[i] != o.k.e[i] || o.vs.e[i] != o.k.e[i])
         refuse(TC_E_EXTENT, n + ": scales must have shape (pages, page_size, heads)");
