@@ -5,7 +5,6 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
-#include <new>
 #include <string>
 
 #include "paged.hpp"
@@ -15,6 +14,7 @@ namespace {
 using tc::set_last_error;
 
 constexpr int64_t kLim = int64_t(1) << 58;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Thrown inside the entry points and turned into a status at their border.
 struct Refusal {
@@ -244,15 +244,18 @@ int launched(int rc) {
   return TC_OK;
 }
 
+// Runs an entry point's body; no exception leaves it.
 template <class F>
 int guarded(F&& f) noexcept {
   try {
-    set_last_error(TC_OK, "");
-    return f();
-  } catch (const Refusal& r) {
-    return set_last_error(r.code, r.why);
-  } catch (const std::bad_alloc&) {
-    return TC_E_ARG;
+    try {
+      set_last_error(TC_OK, "");
+      return f();
+    } catch (const Refusal& r) {
+      return set_last_error(r.code, r.why);
+    }
+  } catch (...) {
+    return TC_E_ARG;  // no memory for the check's own text
   }
 }
 
@@ -366,7 +369,7 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     const int64_t batch = qo.e[0], q_heads = qo.e[1];
     need(qo.e[2] == c.dim, TC_E_EXTENT, "q and the cache differ in head_dim");
     attention_sizes(batch, q_heads, c.heads, c.dim, max_len);
-    need(std::isfinite(scale), TC_E_ARG, "scale must be finite");
+    need(std::isfinite(scale * kLog2e), TC_E_ARG, "scale (and scale * log2 e) must be finite");
     tc::AttentionArgs a{};
     Operand t, l{}, w{}, wo{};
     a.table = table_of("block_table", block_table, table_layout, &t);
@@ -437,7 +440,7 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     a.tile_heads = int32_t(ws.cut.tile_heads);
     a.head_tiles = int32_t(ws.cut.head_tiles);
     a.unit = tc::make_div32(uint32_t(ws.cut.unit_rows));
-    a.scale_log2e = scale * 1.4426950408889634f;
+    a.scale_log2e = scale * kLog2e;
     return launched(tc::launch_paged_attention(a, dtype, c.dtype, stream));
   });
 }

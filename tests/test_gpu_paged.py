@@ -208,6 +208,68 @@ def test_attention_views_and_other_layouts():
     _attend(q.contiguous(), pool, table, lens, page, torch.zeros(3, heads, 300), max_len=130)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_attention_of_many_and_of_long_sequences(kind):
+    """More sequences than lanes of a wave and than runs of rows; one sequence in more parts than lanes; one long
+    sequence among short ones."""
+    gen = torch.Generator().manual_seed(9)
+    lengths = [[int(x) for x in torch.randint(0, 700, (300,), generator=gen)], [70003], [3, 1, 20011, 0, 90, 1],
+               [513] * 70 + [0] * 70 + [1400]]
+    for heads, page, lens in zip((1, 1, 2, 9), (16, 24, 32, 7), lengths):
+        table, pages = R.table_for(lens, page, gen)
+        pool = R.Pool(kind, pages, page, heads, 32, "heads", gen)
+        q = torch.randn(len(lens), 2 * heads, 32, generator=gen).to(torch.bfloat16)
+        say(f"[gpu] {len(lens)} sequences, longest {max(lens)}, {heads} heads, {kind}")
+        _attend(q, pool, table, lens, page, torch.zeros(len(lens), heads, max(lens)) if len(lens) < 300 else None)
+
+
+def test_attention_scales():
+    gen = torch.Generator().manual_seed(10)
+    lens, page = [40, 600], 16
+    table, pages = R.table_for(lens, page, gen)
+    pool = R.Pool("fp16", pages, page, 1, 64, "rows", gen)
+    q = torch.randn(2, 3, 64, generator=gen).to(torch.float16)
+    for scale in (-0.3, 0.0, 1.0, 3.0):
+        say(f"[gpu] scale {scale}")
+        _attend(q, pool, table, lens, page, scale=scale)
+
+
+def test_calls_from_threads_on_separate_streams():
+    import threading
+    jobs, errors = [], []
+    for i in range(6):
+        gen = torch.Generator().manual_seed(90 + i)
+        lens = [50 * i + 1, 900 - 100 * i, 17]
+        table, pages = R.table_for(lens, 16, gen)
+        pool = R.Pool(("bf16", "fp16", "e4m3")[i % 3], pages, 16, 2, 64, "rows", gen)
+        q = torch.randn(3, 8, 64, generator=gen).to(torch.float16 if i % 3 == 1 else torch.bfloat16)
+        ref = R.attention(q, pool, table, lens, 16)
+        jobs.append((pool.on_gpu(), q.cuda(), table.cuda(), _i32(lens), ref))
+    torch.cuda.synchronize()
+
+    def work(cache, q, table, lens, ref):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(8):
+                    w = torch.zeros(3, 2, 912, device="cuda")
+                    out = L.tc_paged_attention(q, cache, table, lens, weights=w, max_len=912)
+                    with pytest.raises(L.TileCopyError):
+                        L.tc_paged_attention(q, cache, table, lens, max_len=-1)
+                    s.synchronize()
+                    _close(out, ref[0], ref[3], "out", q.dtype)
+        except BaseException as e:  # reported below
+            errors.append(repr(e))
+
+    say(f"[gpu] {len(jobs)} threads")
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[:2]
+
+
 def test_attention_equal_calls_give_equal_bits():
     gen = torch.Generator().manual_seed(7)
     lens, page = [5000, 1234], 16
@@ -450,6 +512,9 @@ def test_evict_long_rows_in_one_pool_and_missing_pages():
     w = _weights(2, 1, 70001, gen)
     say("[gpu] evict within one pool")
     _evict_check(pool, table, lens, page, w, None, into_table, page, budget, recent, same_pool=True)
+    say("[gpu] evict from 20001 rows")
+    _evict_check(pool, table, lens, page, w, R.Pool("bf16", pages, page, 1, 32, "rows", fill=0.0), into_table, page, budget, recent,
+                 max_len=20001)
     say("[gpu] evict with a max_len under the lengths")
     _evict_check(pool, table, lens, page, w, R.Pool("bf16", pages, page, 1, 32, "heads", fill=0.0), into_table, page, budget,
                  recent, max_len=801)
@@ -607,3 +672,9 @@ def test_empty_calls():
     L.tc_paged_evict(cache, e(0, 2, dtype=torch.int32), i0, e(0, 2, 32), cache, e(0, 2, dtype=torch.int32), 4)
     for x, y in zip(R.cache_tensors(cache), pool.tensors()):
         _same(x, y, "the cache")
+    none = L.PagedCache(e(0, 16, 2, 64, dtype=torch.bfloat16), e(0, 16, 2, 64, dtype=torch.bfloat16))
+    one = torch.ones(2, 4, 64, device="cuda", dtype=torch.bfloat16)
+    for cols in (1, 100):
+        out = L.tc_paged_attention(one, none, torch.zeros(2, cols, device="cuda", dtype=torch.int32), _i32([16, 9]))
+        assert not out.any()
+        L.tc_paged_append(none, one[:, :2], one[:, :2], torch.zeros(2, cols, device="cuda", dtype=torch.int32), _i32([16, 9]))
