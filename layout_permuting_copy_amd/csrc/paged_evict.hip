@@ -14,6 +14,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// How many lanes below this one a ballot holds.
+__device__ __forceinline__ uint32_t lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0));
+}
+
 // The sum of x[0 .. wave - 1] (WAVES <= 16 values in LDS, one a lane).
 template <int WAVES>
 __device__ __forceinline__ uint32_t sum_below(const uint32_t* x, int wave, int lane) {
@@ -76,6 +81,7 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
   __shared__ uint32_t wave_sum[WAVES], wave_eq[WAVES];
   __shared__ uint32_t found_digit, found_above, found_count;
   uint32_t prefix = 0, mask = 0;
+  bool all = false;
   uint32_t left = uint32_t(want);  // keys still to be found among those that match the prefix
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
@@ -118,15 +124,34 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
     prefix |= found_digit << shift;
     mask |= (bins - 1) << shift;
     left -= found_above;
-    if (found_count == left) break;
+    all = found_count == left;
+    if (all) break;
     __syncthreads();  // found_*, wave_sum and hist are written again
   }
   __syncthreads();
 
-  // keys above the prefix stay, and `left` of those equal to it, the lowest rows first
+  const auto keep = [&](int i, float x, int64_t j) {
+    kept[j * a.kr.sc] = i;
+    if (wo) wo[j * a.wo.sc] = x;
+  };
+  if (all) {
+    // every key with the prefix or above stays
+    uint32_t count = 0;
+    each([&](int, float x, bool in) { count += __popcll(__ballot(in && (weight_key(x) & mask) >= prefix)); });
+    if (lane == 0) wave_sum[wave] = count;
+    __syncthreads();
+    uint32_t before = sum_below<WAVES>(wave_sum, wave, lane);
+    each([&](int i, float x, bool in) {
+      const uint64_t m = __ballot(in && (weight_key(x) & mask) >= prefix);
+      if (m >> lane & 1) keep(i, x, before + lanes_below(m));
+      before += __popcll(m);
+    });
+    return;
+  }
+  // keys above T stay, and `left` of those equal to it, the lowest rows first
   uint32_t gt = 0, eq = 0;
   each([&](int, float x, bool in) {
-    const uint32_t key = weight_key(x) & mask;
+    const uint32_t key = weight_key(x);
     gt += __popcll(__ballot(in && key > prefix));
     eq += __popcll(__ballot(in && key == prefix));
   });
@@ -136,17 +161,12 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
   }
   __syncthreads();
   uint32_t gt_before = sum_below<WAVES>(wave_sum, wave, lane), eq_before = sum_below<WAVES>(wave_eq, wave, lane);
-  const uint64_t below = (uint64_t(1) << lane) - 1;
   each([&](int i, float x, bool in) {
-    const uint32_t key = weight_key(x) & mask;
+    const uint32_t key = weight_key(x);
     const uint64_t g = __ballot(in && key > prefix), e = __ballot(in && key == prefix);
-    const uint32_t eq_rank = eq_before + __popcll(e & below);
+    const uint32_t eq_rank = eq_before + lanes_below(e);
     const uint32_t ties = eq_rank < left ? eq_rank : left;  // kept ties below this row
-    if ((g >> lane & 1) || ((e >> lane & 1) && eq_rank < left)) {
-      const int64_t j = gt_before + __popcll(g & below) + ties;
-      kept[j * a.kr.sc] = i;
-      if (wo) wo[j * a.wo.sc] = x;
-    }
+    if ((g >> lane & 1) || ((e >> lane & 1) && eq_rank < left)) keep(i, x, gt_before + lanes_below(g) + ties);
     gt_before += __popcll(g);
     eq_before += __popcll(e);
   });
