@@ -7,7 +7,7 @@ namespace dev {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRounds = 1;     // rows a lane moves
+constexpr int kAppendRounds = 1;     // rows a lane moves (1, 2, 4: the prompts in 27, 29, 31 us)
 constexpr int kAppendStarts = 2048;  // token_starts kept in LDS
 
 // Eight 2-byte values at p: one 16-byte load, or element loads where rows are not 16-byte aligned.
@@ -84,7 +84,9 @@ __device__ __forceinline__ void store_row(const u32x4& v, int c, bool active, un
 // move eight values each of the key and of the value.  The rows are on their way while the place of each of the
 // workgroup's tokens is found, once for all its heads: its sequence by a binary search of token_starts (in LDS
 // where they fit), then length, page, offset.
-// Bound: HBM for prompts, the latency of starts -> length -> table -> row for single tokens.
+// Bound: HBM for prompts (16665 tokens of 8 heads of 128: 137 MB in 25.6 us, 5.3 TB/s; new rows are read and cache rows
+// written past the caches), the latency of starts -> length -> table -> row otherwise (32 single tokens 2.7 us, 6994
+// tokens of 8 heads of 64 to 8 bits 8.2 us).
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
 __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs a, Div32 heads) {
   constexpr int RPR = kAppendThreads / LPR;         // rows a round

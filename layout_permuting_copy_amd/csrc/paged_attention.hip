@@ -159,12 +159,7 @@ __device__ __forceinline__ Walk walk_lengths(const AttentionArgs& a) {
     const int b = lane * w.per + k;
     if (b < a.table.batch) sum += units_of(paged_len(a.lens, b, a.max_len), a.unit);
   }
-  uint32_t upto = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint32_t o = __shfl_up(upto, d, 64);
-    if (lane >= d) upto += o;
-  }
+  const uint32_t upto = wave_scan(sum);
   w.total = uint32_t(__builtin_amdgcn_readlane(int(upto), 63));
   w.before = upto - sum;
   return w;
@@ -209,7 +204,14 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 // PAGE, the rows known to lie on one page: 16 (a half: its address is scalar, its loads go through a
 // buffer resource), 4 (a lane's value rows of a half) or 1.
 //
-// Bound: HBM (a cache row is read once for all heads of its group).
+// Bound: HBM (a cache row is read once for all heads of its group; FETCH_SIZE counts each byte once).  Measured: one
+// sequence of 131072 rows, 8 heads of 128 bf16 elements under 64 query heads: 537 MB in 83.5 us (6.4 TB/s, where
+// a plain read of 1 GiB reaches 6.1 through the caches and 7.0 past them); 32 of 16384 8-bit rows: 1.11 GB in 174 us
+// (6.4 TB/s); 64 of mixed lengths up to 4096 in pages that hold a row's heads together: 468 MB in 83 us (5.6).  Short
+// calls are a chain of trips to memory: 131 rows take 6.4 us in a graph, where an empty kernel takes 1.6.  Tried and not
+// kept: two tiles ahead of the one computed (the short call 7.1 us, the others level), the next sequence's first
+// tile requested before a segment's end (level), fixed splits of 256 to 2048 rows with a join of all (64 sequences:
+// 106 to 143 us).
 template <bool BF16, bool E4M3, int DP, int HT, int PAGE, bool FULL>
 struct Attend {
   static constexpr bool VBF = BF16 || E4M3;       // type of the second product
@@ -326,8 +328,8 @@ struct Attend {
     if constexpr (E4M3) k.scale = load_scale(ks0, ksp, ksr, pages, t, live);
   }
 
-  // Values are read past the caches: nothing else needs their lines (keys are not, as a line of a
-  // key row is covered by two loads).
+  // Values are read past the caches: nothing else needs their lines (131072 rows: 103 -> 93 us).  Keys are not, as a
+  // line of a key row is covered by two loads (past the caches: 8 sequences with weights 33 -> 38 us).
   __device__ __forceinline__ void load_values(int entry, int t, bool live, Values& v) const {
     const int pages = page_of(entry);
 #pragma unroll
@@ -702,7 +704,7 @@ void paged_attention_kernel(AttentionArgs args) {
 // The parts of one query head of a sequence that was cut, joined: their maxima give each part's factor, sums and
 // outputs are added in a fixed order.  Grid: (sequence or run, query head); those with nothing to join end at
 // once.  32 lanes of four or eight elements, 8 parts at a time and 8 such rounds of loads on their way: the call's
-// time is three trips to memory.
+// time is its launch and three trips to memory (32 parts of 64 heads: 4.9 us; with one round at a time, 10 us).
 template <bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(AttentionArgs a) {
   constexpr int G = kJoinThreads / 32, R = 64 / G;
@@ -777,7 +779,8 @@ __global__ __launch_bounds__(kJoinThreads) void paged_join_kernel(AttentionArgs 
 }
 
 // weights_out[i] = weights[i] + the sum over a cache head's query heads of exp2(logit - maximum) / sum.
-// One lane a row, one workgroup 256 rows of one (sequence, cache head).  Bound: the logits' bytes.
+// One lane a row, one workgroup 256 rows of one (sequence, cache head).  Bound: its launch, and the logits' bytes
+// (28728 rows, 8 heads, groups of 4: 4.0 us; with 1024 rows a workgroup 8.4).
 constexpr int kWeightRows = 256;
 __global__ __launch_bounds__(kWeightRows) void paged_weights_kernel(AttentionArgs a, Div32 heads, Div32 chunks) {
   const uint32_t bh = udiv(blockIdx.x, chunks), chunk = blockIdx.x - bh * chunks.d;
@@ -845,8 +848,12 @@ PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim
   // 32 heads at once for larger groups, where their outputs fit the registers
   c.tile_heads = group > 16 && head_dim <= 128 ? 32 : 16;
   c.head_tiles = (group + c.tile_heads - 1) / c.tile_heads;
+  // a turn of the four waves (units of 64 or 32 rows: 64 sequences of mixed lengths 89 -> 90 or 93 us, others level);
+  // at least two turns a run (one or two: level, four: 16 sequences under one head 22 -> 30 us)
   c.unit_rows = dev::kStep;
   c.least_units = 2;
+  // short caches are not cut: four turns take less than the join's launch (16 sequences, 128 elements: 512 rows
+  // in 9 us uncut, 513 in 12 us cut)
   if (max_len <= 512) {
     c.unit_rows = std::max<int64_t>(dev::kStep, (max_len + dev::kStep - 1) / dev::kStep * dev::kStep);
     c.least_units = 1;
