@@ -436,6 +436,7 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     const int64_t held = t.empty || c.empty ? 0 : std::min<int64_t>(max_len, int64_t(a.table.cols) * c.page_size);
     a.max_len = int32_t(held);
     a.units = ws.cut.units;
+    a.runs = int32_t(ws.cut.runs);
     a.least_units = int32_t(ws.cut.least_units);
     a.tile_heads = int32_t(ws.cut.tile_heads);
     a.head_tiles = int32_t(ws.cut.head_tiles);
