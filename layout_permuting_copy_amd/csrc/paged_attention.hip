@@ -851,15 +851,17 @@ PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim
   // at least two turns a run (one or two: level, four: 16 sequences under one head 22 -> 30 us)
   c.unit_rows = dev::kStep;
   c.least_units = 2;
+  const int64_t pairs = heads * c.head_tiles;
   // short caches are not cut: four turns take less than the join's launch (16 sequences, 128 elements: 512 rows
-  // in 9 us uncut, 513 in 12 us cut)
-  if (max_len <= 512) {
+  // in 9 us uncut, 513 in 12 us cut), and eight turns where every CU has a sequence and head anyway (8 heads of 128,
+  // mixed lengths, uncut and cut: 16 sequences of up to 1000 rows 17 and 16 us, 32 18 and 23, 512 171 and 188; of up
+  // to 2000 rows 32 sequences 31 and 30, 64 58 and 53)
+  if (max_len <= 512 || (max_len <= 1024 && batch * pairs >= dev::kCus)) {
     c.unit_rows = std::max<int64_t>(dev::kStep, (max_len + dev::kStep - 1) / dev::kStep * dev::kStep);
     c.least_units = 1;
   }
   c.units = batch * std::max<int64_t>(1, (max_len + c.unit_rows - 1) / c.unit_rows);
   c.cuts = c.units > batch;
-  const int64_t pairs = heads * c.head_tiles;
   // uncut sequences get a run each, and workgroups that wait their turn hide each other's ends and beginnings (512 of 512
   // rows: 181 us, 206 in one run a CU)
   c.runs = !c.cuts ? batch

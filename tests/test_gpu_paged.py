@@ -223,6 +223,38 @@ def test_attention_of_many_and_of_long_sequences(kind):
         _attend(q, pool, table, lens, page, torch.zeros(len(lens), heads, max(lens)) if len(lens) < 300 else None)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 12, 7])
+@pytest.mark.parametrize("dim", [16, 80, 192])
+def test_attention_reads_no_other_heads_rows(kind, page, dim):
+    """Rows shorter than the kernel's lanes cover, beside a head whose rows are NaN, and at the very end of a pool."""
+    gen = torch.Generator().manual_seed(12)
+    lens = [45, 200]
+    table, pages = R.table_for(lens, page, gen)
+    pool = R.Pool(kind, pages, page, 3, dim, "rows", gen)
+    for x in (pool.k, pool.v):
+        R.bits(x)[:, :, 1] = R.bits(torch.full((1,), float("nan")).to(x.dtype))[0]
+    q = torch.randn(2, 6, dim, generator=gen).to(torch.float16 if kind == "fp16" else torch.bfloat16)
+    say(f"[gpu] NaN in a neighbouring head {kind} page={page} dim={dim}")
+    out, _, _ = _attend(q, pool, table, lens, page, torch.zeros(2, 3, 200))
+    assert bool(out[:, 2:4].isnan().all()) and not bool(out[:, :2].isnan().any()) and not bool(out[:, 4:].isnan().any())
+
+
+@pytest.mark.parametrize("batch", [31, 33, 300])
+def test_attention_around_the_uncut_lengths(batch):
+    """Lengths up to 1024 with and without a sequence and head for every CU: uncut and cut calls."""
+    gen = torch.Generator().manual_seed(13)
+    lens = [int(x) for x in torch.randint(0, 1025, (batch,), generator=gen)]
+    lens[1], lens[2] = 1024, 0
+    heads = 8 if batch < 300 else 1
+    table, pages = R.table_for(lens, 32, gen)
+    pool = R.Pool("bf16", pages, 32, heads, 16, "rows", gen)
+    q = torch.randn(batch, heads, 16, generator=gen).to(torch.bfloat16)
+    for most in (1024, 1025):
+        say(f"[gpu] {batch} sequences, max_len {most}")
+        _attend(q, pool, table, lens, 32, max_len=most)
+
+
 def test_attention_scales():
     gen = torch.Generator().manual_seed(10)
     lens, page = [40, 600], 16
