@@ -188,7 +188,9 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 //                  elements (16 lanes: a whole row) and regroups them by byte permutes.
 //
 // P is held as the sum of two 16-bit values (its rounding and the rest), two products each: the matrix
-// cores are idle nine cycles in ten here, and out is then as exact as fp32 sums of fp32 weights.
+// cores are idle nine cycles in ten here, and out is then as exact as fp32 sums of fp32 weights.  fp16 parts end at
+// 2^-25, which many light rows beside a heavy one would notice: weights (and sums) are 2^15 times as large there until
+// the waves meet.
 // 8-bit rows become 16-bit values in registers (exactly); the key's scale multiplies its row's
 // logits, the value's its row's weights.
 //
@@ -222,6 +224,7 @@ struct Attend {
   static constexpr int VB = VF * EB;              // their bytes: 4, 8, 16 or 32
   static constexpr int VP = VB == 32 ? 16 : VB;   // bytes a load
   static constexpr int VW = VB / 4;
+  static constexpr int RAISE = VBF ? 0 : 15;      // weights are held times 2 to this (at most 2^15, 65504 is fp16's last)
 
   // The element of Q that contraction index (step s, group g, j) stands for.
   static __device__ __forceinline__ int q_element(int s, int g, int j) {
@@ -578,12 +581,13 @@ void paged_attention_kernel(AttentionArgs args) {
             for (int f = 0; f < VF; ++f) o[ht][f] *= shrink;
             m[ht] = top;
           }
+          const float base = ref - float(A::RAISE);
           float e[8];
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              e[4 * u + j] = __builtin_amdgcn_exp2f(s[ht][u][j] - ref);
+              e[4 * u + j] = __builtin_amdgcn_exp2f(s[ht][u][j] - base);
               l[ht] += e[4 * u + j];
               if constexpr (E4M3) e[4 * u + j] *= vs[u][j];
             }
@@ -654,7 +658,7 @@ void paged_attention_kernel(AttentionArgs args) {
         f32x4 all = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < kAttnWaves; ++i) {
-          const float f = __builtin_amdgcn_exp2f(merge_ml[i][0][head] - ref);
+          const float f = __builtin_amdgcn_exp2f(merge_ml[i][0][head] - ref) * (1.0f / float(1 << A::RAISE));
           sum += merge_ml[i][1][head] * f;
           all += *reinterpret_cast<const f32x4*>(&merge_o[i][head][d0]) * f;
         }

@@ -109,8 +109,8 @@ def attention(q, pool, table, lens, page, scale=None):
     factor and the exponential's own error (2 units, 4 e) beside it.  A weight is off by the relative amount
     exp(dx) - 1, from its own logit and from the row's maximum and sum: 2 dx + 16 e.  Sums over rows run to
     a depth of n / 16 + 96 additions (waves, tiles, splits), each off by e of the sum of magnitudes.  The weights
-    enter the second product as two 16-bit values: bf16 leaves 2^-17 of the weight, fp16 2^-22 of it or 2^-25 of
-    the row's maximum, whose weight before division is 1."""
+    enter the second product as two 16-bit values: bf16 leaves 2^-17 of the weight, fp16 2^-22 of it or 2^-40 of
+    the row's maximum (whose weight before division is 2^15)."""
     scale = q.shape[2] ** -0.5 if scale is None else scale
     batch, heads_q, dim = q.shape
     heads = pool.k.shape[2]
@@ -145,7 +145,7 @@ def attention(q, pool, table, lens, page, scale=None):
             mag = p @ v[:, h].abs()
             t_out[b, hq] = mag * (rel + 2.0 ** -17)
             if q.dtype == torch.float16 and pool.kind != "e4m3":
-                t_out[b, hq] += 2.0 ** -25 * torch.exp(x.max() - total) * v[:, h].abs().sum(0)
+                t_out[b, hq] += 2.0 ** -40 * torch.exp(x.max() - total) * v[:, h].abs().sum(0)
             t_lse[b, hq] = dx + 16 * STEP32 + depth + 4 * STEP32 * (abs(total) + abs(x).max())
             t_w[b, h, at] += p * rel
     return out, lse, weight, t_out, t_lse, t_w

@@ -176,6 +176,25 @@ def test_attention_lowest_values_and_sharp_rows():
         _same(out[1, 0], pool.v[int(table[1, 2]), 5, 0], "the row that takes all the weight")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_attention_of_many_light_rows_beside_a_heavy_one(kind):
+    """One row whose weight is e^17.5 times that of each of 8000 others, which hold all of out."""
+    gen = torch.Generator().manual_seed(14)
+    lens, page = [8001] * 4, 16
+    table, pages = R.table_for(lens, page, gen)
+    pool = R.Pool(kind, pages, page, 1, 64, "rows", gen)
+    pool.k.zero_()
+    pool.v.fill_(1.0)
+    for b in range(4):
+        pool.k[int(table[b, 0]), b, 0, 0] = 17.5
+        pool.v[int(table[b, 0]), b, 0] = 0.0
+    q = torch.zeros(4, 2, 64).to(R.DT[kind])
+    q[:, :, 0] = 1.0
+    for most in (1000, 8001):
+        say(f"[gpu] light rows {kind}, {most} rows")
+        _attend(q, pool, table, [min(n, most) for n in lens], page, scale=1.0)
+
+
 def test_attention_views_and_other_layouts():
     """q and out as slices, a table with strides, a strided lse, weights of one buffer grown in place, a small max_len."""
     gen = torch.Generator().manual_seed(6)
