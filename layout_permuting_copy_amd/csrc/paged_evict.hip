@@ -6,12 +6,11 @@ namespace dev {
 
 constexpr int kBins = 2048;  // histogram bins: 11 bits of a key
 
-// An unsigned integer that orders weights as numbers: equal zeros, any NaN above all.
+// An unsigned integer that orders weights as numbers: equal zeros, any NaN above all.  The lowest, -infinity's, is
+// 0x007fffff.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, w);
-  if (w != w) return 0xffffffffu;
-  if ((u << 1) == 0) return 0x80000000u;
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __builtin_bit_cast(uint32_t, w + 0.0f);  // -0 + 0 = 0
+  return w != w ? 0xffffffffu : u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
 
 // How many lanes below this one a ballot holds.
@@ -33,10 +32,11 @@ __device__ __forceinline__ uint32_t sum_below(const uint32_t* x, int wave, int l
 // those digits stays.  Every wave owns a stretch of the rows, so a walk in order needs only the waves' counts to
 // place what it keeps.
 //
-// KEYS: weights a lane holds in registers (one read of the weights; THREADS * KEYS rows at most), or 0: every
-// pass reads them again, from the caches.  HISTS: copies of the histogram, one for every HISTS-th wave, so that
-// fewer lanes add to one bin.  Bound: trips to memory, barriers and LDS atomics, one workgroup's (8 heads of 2049
-// rows 6.9 us, 128 of up to 16384 rows 20 us; with the weights read again by every pass 10 and 33 us).
+// KEYS: weights a lane holds in registers, with their keys (one read of the weights; THREADS * KEYS rows at most), or
+// 0: every pass reads them again, from the caches.  HISTS: copies of the histogram, one for every HISTS-th wave, so that
+// fewer lanes add to one bin.  Bound: trips to memory, barriers, LDS atomics and, with many rows, the vector
+// instructions of one workgroup's walks (8 heads of 2049 rows 6.6 us, 128 of up to 16384 rows 15.4 us; with the keys made
+// again by every walk 20 us, with the weights read again by every pass 33 us).
 template <int THREADS, int KEYS, int HISTS>
 __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div32 heads) {
   constexpr int WAVES = THREADS / 64, BPT = kBins / THREADS;  // bins a thread sums
@@ -60,6 +60,7 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
   const int seg = ((cand + WAVES - 1) / WAVES + 63) / 64 * 64;  // at most 64 * KEYS, if those are held
   const int lo = wave * seg, hi = lo + seg < cand ? lo + seg : cand;
   float held[KEYS ? KEYS : 1];
+  uint32_t key_held[KEYS ? KEYS : 1];
 #pragma unroll
   for (int k = 0; k < KEYS; ++k) held[k] = lo + 64 * k + lane < hi ? w[(lo + 64 * k + lane) * a.w.sc] : 0.0f;
   for (int j = tid; j < a.recent; j += THREADS) {
@@ -67,14 +68,19 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
     if (wo) wo[(want + j) * a.wo.sc] = w[(cand + j) * a.w.sc];
   }
   if (want == 0) return;
-  // f(row, weight, whether the lane has one) over the wave's rows, 64 at a time, in order
+#pragma unroll
+  for (int k = 0; k < KEYS; ++k) key_held[k] = lo + 64 * k + lane < hi ? weight_key(held[k]) : 0u;
+  // f(row, weight, key) over the wave's rows, 64 at a time, in order; lanes past them have key 0, which no weight has
   const auto each = [&](auto f) {
     if constexpr (KEYS > 0) {
 #pragma unroll
       for (int k = 0; k < KEYS; ++k)
-        if (lo + 64 * k < hi) f(lo + 64 * k + lane, held[k], lo + 64 * k + lane < hi);
+        if (lo + 64 * k < hi) f(lo + 64 * k + lane, held[k], key_held[k]);
     } else {
-      for (int i = lo + lane; i - lane < hi; i += 64) f(i, i < hi ? w[i * a.w.sc] : 0.0f, i < hi);
+      for (int i = lo + lane; i - lane < hi; i += 64) {
+        const float x = i < hi ? w[i * a.w.sc] : 0.0f;
+        f(i, x, i < hi ? weight_key(x) : 0u);
+      }
     }
   };
 
@@ -90,9 +96,8 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
     const uint32_t bins = pass == 2 ? 1024 : 2048;
     for (int i = tid; i < HISTS * kBins / 4; i += THREADS) reinterpret_cast<u32x4*>(&hist[0][0])[i] = u32x4{};
     __syncthreads();
-    each([&](int, float x, bool in) {
-      const uint32_t key = weight_key(x);
-      if (in && (key & mask) == prefix) atomicAdd(&hist[wave % HISTS][(key >> shift) & (bins - 1)], 1u);
+    each([&](int, float, uint32_t key) {
+      if (pass ? (key & mask) == prefix : key != 0) atomicAdd(&hist[wave % HISTS][(key >> shift) & (bins - 1)], 1u);
     });
     __syncthreads();
     // thread t sums the BPT bins below kBins - BPT * t; the wanted bin is where the count from the top first
@@ -131,19 +136,26 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
   }
   __syncthreads();
 
-  const auto keep = [&](int i, float x, int64_t j) {
-    kept[j * a.kr.sc] = i;
-    if (wo) wo[j * a.wo.sc] = x;
+  // (64-bit products a row would take as long as the rest of the walk)
+  const bool dense = a.kr.sc == 1 && (!wo || a.wo.sc == 1);
+  const auto keep = [&](int i, float x, uint32_t j) {
+    if (dense) {
+      kept[j] = i;
+      if (wo) wo[j] = x;
+    } else {
+      kept[j * a.kr.sc] = i;
+      if (wo) wo[j * a.wo.sc] = x;
+    }
   };
   if (all) {
     // every key with the prefix or above stays
     uint32_t count = 0;
-    each([&](int, float x, bool in) { count += __popcll(__ballot(in && (weight_key(x) & mask) >= prefix)); });
+    each([&](int, float, uint32_t key) { count += __popcll(__ballot(key >= prefix)); });
     if (lane == 0) wave_sum[wave] = count;
     __syncthreads();
     uint32_t before = sum_below<WAVES>(wave_sum, wave, lane);
-    each([&](int i, float x, bool in) {
-      const uint64_t m = __ballot(in && (weight_key(x) & mask) >= prefix);
+    each([&](int i, float x, uint32_t key) {
+      const uint64_t m = __ballot(key >= prefix);
       if (m >> lane & 1) keep(i, x, before + lanes_below(m));
       before += __popcll(m);
     });
@@ -151,10 +163,9 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
   }
   // keys above T stay, and `left` of those equal to it, the lowest rows first
   uint32_t gt = 0, eq = 0;
-  each([&](int, float x, bool in) {
-    const uint32_t key = weight_key(x);
-    gt += __popcll(__ballot(in && key > prefix));
-    eq += __popcll(__ballot(in && key == prefix));
+  each([&](int, float, uint32_t key) {
+    gt += __popcll(__ballot(key > prefix));
+    eq += __popcll(__ballot(key == prefix));
   });
   if (lane == 0) {
     wave_sum[wave] = gt;
@@ -162,9 +173,8 @@ __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div3
   }
   __syncthreads();
   uint32_t gt_before = sum_below<WAVES>(wave_sum, wave, lane), eq_before = sum_below<WAVES>(wave_eq, wave, lane);
-  each([&](int i, float x, bool in) {
-    const uint32_t key = weight_key(x);
-    const uint64_t g = __ballot(in && key > prefix), e = __ballot(in && key == prefix);
+  each([&](int i, float x, uint32_t key) {
+    const uint64_t g = __ballot(key > prefix), e = __ballot(key == prefix);
     const uint32_t eq_rank = eq_before + lanes_below(e);
     const uint32_t ties = eq_rank < left ? eq_rank : left;  // kept ties below this row
     if ((g >> lane & 1) || ((e >> lane & 1) && eq_rank < left)) keep(i, x, gt_before + lanes_below(g) + ties);

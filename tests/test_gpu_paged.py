@@ -551,6 +551,36 @@ def test_evict_equal_weights_keep_the_lowest_rows():
             _evict_check(pool, table, lens, 16, w, into, into_table, 16, budget, recent)
 
 
+def test_evict_of_infinite_weights_into_strided_rows():
+    """Weights of both infinities, zeros of both signs and the lowest and highest numbers; kept and weights_out with
+    strides between their columns give what dense ones do."""
+    gen = torch.Generator().manual_seed(15)
+    page, heads = 16, 2
+    for lens, budget, recent in (([700, 90], 64, 7), ([3000, 1], 900, 0), ([40000, 20000], 5000, 100)):
+        table, pages = R.table_for(lens, page, gen)
+        into_table, into_pages = R.table_for([min(n, budget) for n in lens], page, gen)
+        pool = R.Pool("bf16", pages, page, heads, 16, "rows", gen)
+        into = R.Pool("bf16", into_pages, page, heads, 16, "rows", fill=0.0)
+        w = torch.randn(2, heads, max(lens), generator=gen)
+        pick = torch.randint(0, 40, w.shape, generator=gen)
+        for i, x in enumerate((math.inf, -math.inf, 0.0, -0.0, 3.4e38, -3.4e38, 1e-42, -1e-42)):
+            w[pick == i] = x
+        w[1, 1] = -math.inf
+        say(f"[gpu] infinite weights lens={lens}")
+        _evict_check(pool, table, lens, page, w, into, into_table, page, budget, recent)
+        got = []
+        for step in (1, 3):
+            kept = torch.full((2, heads, budget, step), 5, dtype=torch.int32, device="cuda")
+            wo = torch.full((2, heads, budget, step), 5.0, device="cuda")
+            L.tc_paged_evict(pool.on_gpu(), table.cuda(), _i32(lens), w.cuda(), into.on_gpu(), into_table.cuda(), budget, recent,
+                             max_len=max(lens), weights_out=wo[..., 0], kept=kept[..., 0])
+            torch.cuda.synchronize()
+            assert bool((kept[..., 1:] == 5).all()) and bool((wo[..., 1:] == 5).all())
+            got.append((kept[..., 0].cpu(), wo[..., 0].cpu()))
+        assert torch.equal(got[0][0], got[1][0])
+        _same(got[1][1], got[0][1], "weights")
+
+
 def test_evict_long_rows_in_one_pool_and_missing_pages():
     """Into other pages of the same pool; pages missing on either side; a max_len under the lengths; a long sequence."""
     gen = torch.Generator().manual_seed(71)
