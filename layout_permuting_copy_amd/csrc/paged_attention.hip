@@ -210,7 +210,7 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 // sequence of 131072 rows, 8 heads of 128 bf16 elements under 64 query heads: 537 MB in 83.5 us (6.4 TB/s, where
 // a plain read of 1 GiB reaches 6.1 through the caches and 7.0 past them); 32 of 16384 8-bit rows: 1.11 GB in 174 us
 // (6.4 TB/s); 64 of mixed lengths up to 4096 in pages that hold a row's heads together: 468 MB in 83 us (5.6).  Short
-// calls are a chain of trips to memory: 131 rows take 6.4 us in a graph, where an empty kernel takes 1.6.  Tried and not
+// calls are a chain of trips to memory: 131 rows take 6.3 us in a graph, where an empty kernel takes 1.6.  Tried and not
 // kept: two tiles ahead of the one computed (the short call 7.1 us, the others level), the next sequence's first
 // tile requested before a segment's end (level), fixed splits of 256 to 2048 rows with a join of all (64 sequences:
 // 106 to 143 us).
@@ -648,7 +648,10 @@ void paged_attention_kernel(AttentionArgs args) {
               f32x4{o[ht][f][i], o[ht][f + 1][i], o[ht][f + 2][i], o[ht][f + 3][i]};
       __syncthreads();
       const int d0 = tid % (DP / 4) * 4;
-      for (int head = tid / (DP / 4); head < 16; head += kAttnThreads / (DP / 4)) {
+      constexpr int at_once = kAttnThreads / (DP / 4);
+#pragma unroll
+      for (int head0 = 0; head0 < 16; head0 += at_once) {
+        const int head = head0 + tid / (DP / 4);
         const int hg = g0 + 16 * ht + head;
         if (hg >= e.group || (!FULL && d0 >= e.head_dim)) continue;
         float mx = -kInf, sum = 0.0f;
