@@ -404,14 +404,15 @@ int tc_paged_append(const tc_paged_cache* cache, const void* k_new, const tc_lay
  * Sums, maxima and products accumulate in fp32, out is rounded once.  No row, or none with x_i above
  * -infinity: out = 0, lse = -infinity.  An infinite value under a weight makes its element of out NaN (values
  * are multiplied by weights held in two parts).  Equal calls give equal bits; where a sequence's rows are cut
- * between workgroups, and with it the last bits of its sums, depends on the whole batch.  Rows past n and rows on no page are never used, whatever
- * they hold.  lse (batch, q_heads), fp32, may be NULL.  weights_out (batch, heads, capacity >= max_len), fp32, may be NULL:
- * receives weights[b][h][i] + the sum of p_i over the head's group, for i < n; weights (the same shape)
- * may be weights_out itself (sums grow in place) or not overlap it; rows from n on are left as they are.
+ * between workgroups, and with it the last bits of its sums, depends on the whole batch and max_len.  Rows past n and
+ * rows on no page are never used, whatever they hold.  lse (batch, q_heads), fp32, may be NULL.  weights_out (batch,
+ * heads, capacity >= max_len), fp32, may be NULL: receives weights[b][h][i] + the sum of p_i over the head's group,
+ * for i < n; weights (the same shape) may be weights_out itself (sums grow in place) or not overlap it; rows from n on
+ * are left as they are.
  * workspace: tc_paged_attention_workspace(...) bytes of device memory, 16-byte aligned, used until
  * the call's kernels end and by no other call meanwhile; may be NULL where that is 0.
- * Errors: as above, TC_E_RANGE (q_heads above 65535, sizes the kernels cannot count); TC_E_ARG (workspace too small, bad scale), TC_E_ALIAS (an output overlaps
- * an input).
+ * Errors: as above, TC_E_RANGE (q_heads above 65535, sizes the kernels or a launch cannot count); TC_E_ARG (workspace
+ * too small, bad scale), TC_E_ALIAS (an output overlaps an input).
  */
 int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layout* q_layout, void* out,
                        const tc_layout* out_layout, int dtype, const int32_t* block_table,

@@ -109,7 +109,10 @@ PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim
 // Columns a row of the logits workspace holds: max_len rounded up to whole tiles.
 int64_t paged_logit_row(int64_t max_len);
 
-// Launchers: TC_OK, or TC_E_ARG where no kernel instance matches.  `dtype` is that of the new rows or of
+// A launch counts its lanes in 32 bits.
+constexpr bool launchable(int64_t workgroups, int64_t threads) { return workgroups * threads < int64_t(1) << 32; }
+
+// Launchers: TC_OK, or TC_E_RANGE, and nothing launched, where a grid would be too large.  `dtype` is that of the new rows or of
 // q, `cache_dtype` the pool's; `wide`: new rows take 16-byte loads.
 int launch_paged_append(const AppendArgs& a, int dtype, int cache_dtype, bool wide, void* stream);
 int launch_paged_attention(const AttentionArgs& a, int dtype, int cache_dtype, void* stream);

@@ -238,7 +238,7 @@ void apart(const char* what, const Operand& a, const Operand& b) {
 }
 
 int launched(int rc) {
-  if (rc != TC_OK) refuse(rc, "no kernel instance for these sizes");
+  if (rc != TC_OK) refuse(rc, "more rows than one launch takes");
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) refuse(TC_E_HIP, std::string("kernel launch failed: ") + hipGetErrorString(e));
   return TC_OK;

@@ -169,15 +169,17 @@ __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs
 }
 
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
-void launch(const AppendArgs& a, hipStream_t s) {
+int launch(const AppendArgs& a, hipStream_t s) {
   const int64_t per = kAppendThreads / LPR * kAppendRounds;
   const int64_t wgs = (a.tokens * a.heads + per - 1) / per;
+  if (!launchable(wgs, kAppendThreads)) return TC_E_RANGE;
   hipLaunchKernelGGL((paged_append_kernel<BF16, E4M3, WIDE, LPR>), dim3(uint32_t(wgs)), dim3(kAppendThreads), 0, s, a,
                      make_div32(uint32_t(a.heads)));
+  return TC_OK;
 }
 
 template <bool BF16, bool E4M3, bool WIDE>
-void by_lanes(const AppendArgs& a, hipStream_t s) {
+int by_lanes(const AppendArgs& a, hipStream_t s) {
   const int lanes = a.head_dim / 8;
   if (lanes <= 2) return launch<BF16, E4M3, WIDE, 2>(a, s);
   if (lanes <= 4) return launch<BF16, E4M3, WIDE, 4>(a, s);
@@ -187,7 +189,7 @@ void by_lanes(const AppendArgs& a, hipStream_t s) {
 }
 
 template <bool E4M3>
-void by_type(const AppendArgs& a, int dtype, bool wide, hipStream_t s) {
+int by_type(const AppendArgs& a, int dtype, bool wide, hipStream_t s) {
   if constexpr (!E4M3) return wide ? by_lanes<true, E4M3, true>(a, s) : by_lanes<true, E4M3, false>(a, s);  // bits either way
   else if (dtype == TC_BF16) return wide ? by_lanes<true, E4M3, true>(a, s) : by_lanes<true, E4M3, false>(a, s);
   else return wide ? by_lanes<false, E4M3, true>(a, s) : by_lanes<false, E4M3, false>(a, s);
@@ -198,11 +200,7 @@ void by_type(const AppendArgs& a, int dtype, bool wide, hipStream_t s) {
 int launch_paged_append(const AppendArgs& a, int dtype, int cache_dtype, bool wide, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (a.tokens * a.heads > (int64_t(1) << 30)) return TC_E_RANGE;
-  if (cache_dtype == TC_E4M3)
-    dev::by_type<true>(a, dtype, wide, s);
-  else
-    dev::by_type<false>(a, dtype, wide, s);
-  return TC_OK;
+  return cache_dtype == TC_E4M3 ? dev::by_type<true>(a, dtype, wide, s) : dev::by_type<false>(a, dtype, wide, s);
 }
 
 }  // namespace tc

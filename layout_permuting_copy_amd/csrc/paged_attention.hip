@@ -883,13 +883,14 @@ int launch_paged_attention(const AttentionArgs& in, int dtype, int cache_dtype, 
   AttentionArgs a = in;
   const int64_t rows = int64_t(a.table.batch) * a.heads;
   const int64_t chunks = (int64_t(a.max_len) + dev::kWeightRows - 1) / dev::kWeightRows;
-  if (rows * chunks >= int64_t(1) << 31) return TC_E_RANGE;
+  if (a.weights_out && !launchable(rows * chunks, dev::kWeightRows)) return TC_E_RANGE;
   const int dp = dev::padded_dim(a.head_dim);
   const int64_t pairs = int64_t(a.heads) * a.head_tiles;
   if (a.parts)
     a.runs = int32_t(runs_of(a.units, a.least_units, pairs,
                              dev::resident_workgroups(dp, cache_dtype == TC_E4M3, a.tile_heads / 16,
                                                       dev::pages_of_16(a.pool) && a.head_dim == dp)));
+  if (!launchable(a.runs * pairs, dev::kAttnThreads)) return TC_E_RANGE;
   a.workgroups = int32_t(a.runs * pairs);
   a.pairs_div = make_div32(uint32_t(pairs));
   a.heads_div = make_div32(uint32_t(a.heads));

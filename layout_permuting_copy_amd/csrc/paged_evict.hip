@@ -242,17 +242,15 @@ __global__ __launch_bounds__(kCopyThreads) void paged_move_kernel(EvictArgs a, D
 }
 
 template <bool E4M3, int LPR>
-int move(const EvictArgs& a, int most, hipStream_t s) {
+void move(const EvictArgs& a, int most, hipStream_t s) {
   constexpr int per = kCopyThreads / LPR * kCopyRounds;
   const int64_t chunks = (int64_t(most) + per - 1) / per, wgs = chunks * a.table.batch * a.heads;
-  if (wgs >= int64_t(1) << 31) return TC_E_RANGE;
   hipLaunchKernelGGL((paged_move_kernel<E4M3, LPR>), dim3(uint32_t(wgs)), dim3(kCopyThreads), 0, s, a,
                      make_div32(uint32_t(a.heads)), make_div32(uint32_t(chunks)));
-  return TC_OK;
 }
 
 template <bool E4M3>
-int move_rows(const EvictArgs& a, int most, hipStream_t s) {
+void move_rows(const EvictArgs& a, int most, hipStream_t s) {
   const int lanes = a.row_bytes / 16;
   if (lanes <= 1) return move<E4M3, 1>(a, most, s);
   if (lanes <= 2) return move<E4M3, 2>(a, most, s);
@@ -267,8 +265,9 @@ int move_rows(const EvictArgs& a, int most, hipStream_t s) {
 int launch_paged_evict(const EvictArgs& a, int cache_dtype, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int most = a.budget < a.max_len ? a.budget : a.max_len;
-  // the move's grid has to fit before anything is launched (8 rows a workgroup at the widest rows)
-  if ((int64_t(most) / 8 + 1) * a.table.batch * a.heads >= int64_t(1) << 31) return TC_E_RANGE;
+  // both grids have to fit before anything is launched (the move's: 8 rows a workgroup at the widest rows)
+  const int64_t rows = int64_t(a.table.batch) * a.heads;
+  if (!launchable(rows, 1024) || !launchable((int64_t(most) / 8 + 1) * rows, dev::kCopyThreads)) return TC_E_RANGE;
   if (a.max_len <= 1024)
     dev::select<256, 4, 1>(a, s);
   else if (a.max_len <= 4096)
@@ -280,7 +279,11 @@ int launch_paged_evict(const EvictArgs& a, int cache_dtype, void* stream) {
   else
     dev::select<1024, 0, 4>(a, s);
   if (most == 0) return TC_OK;
-  return cache_dtype == TC_E4M3 ? dev::move_rows<true>(a, most, s) : dev::move_rows<false>(a, most, s);
+  if (cache_dtype == TC_E4M3)
+    dev::move_rows<true>(a, most, s);
+  else
+    dev::move_rows<false>(a, most, s);
+  return TC_OK;
 }
 
 }  // namespace tc

@@ -120,6 +120,14 @@ BIG = 1 << 59
     (L.TC_E_ALIAS, "input", lambda: _evict(lens_out=BASE + (7 << 20))),
     (L.TC_E_ALIAS, "input", lambda: _evict(wo=BASE + (22 << 20))),
     (L.TC_E_NULL, "kept", lambda: _evict(kept=None)),
+    (L.TC_E_RANGE, "one launch", lambda: _append(new=(1 << 28, HEADS, DIM), k_stride=(0, DIM, 1), starts=BASE + (8 << 20))),
+    (L.TC_E_RANGE, "one launch", lambda: _attend(q_shape=(1 << 23, 4, DIM), q=1 << 40, out=1 << 42, lens=1 << 44, table=(1 << 23, 4))),
+    (L.TC_E_RANGE, "one launch", lambda: _attend(_cache(shape=(PAGES, PAGE, 1, DIM)), q_shape=(1 << 12, 1, DIM), q=1 << 40, out=1 << 42,
+                                                 lens=1 << 44, table=(1 << 12, 1 << 16), max_len=1 << 20, w=1 << 50, wo=1 << 50,
+                                                 w_shape=(1 << 12, 1, 1 << 20), work=1 << 52, work_bytes=1 << 40)),
+    (L.TC_E_RANGE, "one launch", lambda: _evict(table=(1 << 23, 4), dst_table=(1 << 23, 4), kept=1 << 40, lens_out=1 << 42,
+                                                kept_shape=(1 << 23, HEADS, 32), w=1 << 44, w_shape=(1 << 23, HEADS, 64), lens=1 << 46,
+                                                dst=_cache(k=1 << 47, v=1 << 48))),
 ])
 def test_refusals(want, word, call):
     assert call() == want, L.tc_last_error()
