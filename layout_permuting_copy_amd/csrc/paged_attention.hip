@@ -581,13 +581,13 @@ void paged_attention_kernel(AttentionArgs args) {
             for (int f = 0; f < VF; ++f) o[ht][f] *= shrink;
             m[ht] = top;
           }
-          const float base = ref - float(A::RAISE);
           float e[8];
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              e[4 * u + j] = __builtin_amdgcn_exp2f(s[ht][u][j] - base);
+              // (raised after the difference, which rounds to no more than 0: ref - 15 would be any of its neighbours from 2^24 on)
+              e[4 * u + j] = __builtin_amdgcn_exp2f(s[ht][u][j] - ref) * float(1 << A::RAISE);
               l[ht] += e[4 * u + j];
               if constexpr (E4M3) e[4 * u + j] *= vs[u][j];
             }
