@@ -403,7 +403,7 @@ int tc_paged_append(const tc_paged_cache* cache, const void* k_new, const tc_lay
  *
  * Sums, maxima and products accumulate in fp32, out is rounded once.  No row, or none with x_i above
  * -infinity: out = 0, lse = -infinity.  An infinite value under a weight makes its element of out NaN (values
- * are multiplied by weights held in two parts).  Equal calls give equal bits; where a sequence's rows are cut
+ * are multiplied by weights held in parts).  Equal calls give equal bits; where a sequence's rows are cut
  * between workgroups, and with it the last bits of its sums, depends on the whole batch and max_len.  Rows past n and
  * rows on no page are never used, whatever they hold.  lse (batch, q_heads), fp32, may be NULL.  weights_out (batch,
  * heads, capacity >= max_len), fp32, may be NULL: receives weights[b][h][i] + the sum of p_i over the head's group,

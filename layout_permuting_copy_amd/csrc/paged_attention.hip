@@ -187,10 +187,12 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 //                  For V^T lane (r, g) loads, of those eight rows, the same DP / 16 neighbouring
 //                  elements (16 lanes: a whole row) and regroups them by byte permutes.
 //
-// P is held as the sum of two 16-bit values (its rounding and the rest), two products each: the matrix
-// cores are idle nine cycles in ten here, and out is then as exact as fp32 sums of fp32 weights.  fp16 parts end at
-// 2^-25, which many light rows beside a heavy one would notice: weights (and sums) are 2^15 times as large there until
-// the waves meet.
+// P is held as the sum of 16-bit values (its rounding, the rest's rounding, ...), a product each, the matrix cores being
+// mostly idle.  Three bf16 values hold all 24 bits of an fp32 weight; two would leave 2^-18 of it, which shows where
+// values cancel (the third costs 0.2 us of 6.3 of 131 rows, 0.5 of 88 of the batch, 1.2 of 187 of the 8-bit rows).  Two fp16
+// values hold 22 bits: what they leave is no more than the rounding of a logit of 4 does (a third would cost 0.4 of 24.5
+// us).  fp16 parts end at 2^-25, which many light rows beside a heavy one would notice: weights (and sums) are 2^15 times as
+// large there until the waves meet.
 // 8-bit rows become 16-bit values in registers (exactly); the key's scale multiplies its row's
 // logits, the value's its row's weights.
 //
@@ -224,6 +226,7 @@ struct Attend {
   static constexpr int VB = VF * EB;              // their bytes: 4, 8, 16 or 32
   static constexpr int VP = VB == 32 ? 16 : VB;   // bytes a load
   static constexpr int VW = VB / 4;
+  static constexpr int PARTS = VBF ? 3 : 2;   // 16-bit values that hold a weight
   static constexpr int RAISE = VBF ? 0 : 15;      // weights are held times 2 to this (at most 2^15, 65504 is fp16's last)
 
   // The element of Q that contraction index (step s, group g, j) stands for.
@@ -563,8 +566,8 @@ void paged_attention_kernel(AttentionArgs args) {
           }
         }
 
-        // online softmax, and P^T in B's layout as two 16-bit parts
-        u32x4 hi[HT], lo[HT];
+        // online softmax, and P^T in B's layout as 16-bit parts
+        u32x4 part[HT][A::PARTS];
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
           float top = m[ht];
@@ -593,8 +596,13 @@ void paged_attention_kernel(AttentionArgs args) {
             }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            hi[ht][i] = pack2<VBF>(e[2 * i], e[2 * i + 1]);
-            lo[ht][i] = pack2<VBF>(e[2 * i] - low_half<VBF>(hi[ht][i]), e[2 * i + 1] - high_half<VBF>(hi[ht][i]));
+            float x = e[2 * i], y = e[2 * i + 1];
+#pragma unroll
+            for (int k = 0; k < A::PARTS; ++k) {
+              const uint32_t w = part[ht][k][i] = pack2<VBF>(x, y);
+              x -= low_half<VBF>(w);
+              y -= high_half<VBF>(w);
+            }
           }
         }
 
@@ -614,8 +622,8 @@ void paged_attention_kernel(AttentionArgs args) {
           }
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
-            o[ht][f] = mfma<VBF>(y, hi[ht], o[ht][f]);
-            o[ht][f] = mfma<VBF>(y, lo[ht], o[ht][f]);
+#pragma unroll
+            for (int k = 0; k < A::PARTS; ++k) o[ht][f] = mfma<VBF>(y, part[ht][k], o[ht][f]);
           }
         }
       }

@@ -79,3 +79,57 @@ def test_attention_of_logits_far_from_zero(kind, sign, rows):
             # lse: the logit times log2 e and back, each factor and product off by half a step of fp32
             x = sign * 2.0 ** power + math.log(equal)
             assert bool(((lse.cpu().double() - x).abs() <= 6 * R.STEP32 * abs(x)).all()), (lse, x)
+
+
+def _two_parts(e):
+    """e as the sum of two bf16 values, its rounding and the rest's."""
+    hi = e.to(torch.float32).to(torch.bfloat16).double()
+    return hi + (e - hi).to(torch.float32).to(torch.bfloat16).double()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "bf16-e4m3", "fp16-e4m3"])
+@pytest.mark.parametrize("group", [1, 20])
+def test_attention_weights_have_the_precision_of_fp32(kind, group):
+    """A row whose weight two bf16 values hold worst, and three rows of weight e^0 that cancel it down to less than 2^-10:
+    out is then as far off as its weights and sums are.
+
+    With e = 2^-24 and mag = sum p |v|: a logit of at most 1/4 is off by e / 2, its base-2 exponential by 2 e of its own, and
+    a scale of the values adds e: 4 e of the row's weight, which holds half of mag.  The row enters the sums in at most three
+    parts, the others (weight 1) in one: 6 additions of partial sums under half of mag, off by 2 e each where the matrix unit
+    truncates.  The division is off by 2 e of out, which is small.  2 + 6 = 8 e of mag, and 12 with what those round to.  Two
+    bf16 values leave 2^-17.7 of the row's weight, 39 e of mag."""
+    kinds = kind.split("-")
+    dt, kv, dim, page, main, fix = R.DT[kinds[0]], kinds[-1], 64, 16, 1, 3
+    gen = torch.Generator().manual_seed(21)
+    x = -torch.arange(1, 257, dtype=torch.float64) / 1024.0
+    e = torch.exp(x)
+    lost = (e - _two_parts(e)) / e
+    worst = torch.argsort(lost, descending=True)[:main]
+    x = torch.cat([x[worst], torch.zeros(fix, dtype=torch.float64)])
+    e = torch.exp(x)
+    n = main + fix
+    pool = R.Pool(kv, 1, page, 1, dim, "rows", fill=0.0)
+    if kv == "e4m3":
+        pool.k[0, :n, 0, 0] = torch.tensor(-1.0).to(pool.k.dtype)
+        pool.ks.fill_(0.0)
+        pool.ks[0, :n, 0] = -x.float()
+        pool.vs.fill_(1.0)
+    else:
+        pool.k[0, :n, 0, 0] = x.to(pool.k.dtype)
+    v = torch.zeros(n, dim, dtype=torch.float64)
+    to = lambda y: y.float().to(pool.v.dtype).float().double()
+    v[:main] = to(16.0 + 8.0 * torch.rand(main, dim, generator=gen).double())
+    for i in range(main, n):
+        v[i] = to(-(e[:i, None] * v[:i]).sum(0))
+    pool.v[0, :n, 0] = v.float().to(pool.v.dtype)
+    p = e / e.sum()
+    want, mag = p @ v, p @ v.abs()
+    assert bool((want.abs() <= mag * 2.0 ** -10).all())
+    q = torch.zeros(1, group, dim)
+    q[..., 0] = 1.0
+    say(f"[gpu] weights of {kind}, group {group}")
+    out = L.tc_paged_attention(q.to(dt).cuda(), pool.on_gpu(), _i32([[0]]), _i32([n]), scale=1.0)
+    off = (out[0].cpu().double() - want).abs()
+    tol = 12 * R.STEP32 * mag + _half_step(dt, want, 12 * R.STEP32 * mag)
+    say(f"[gpu] off by at most 2^{math.log2(float((off / mag).max()) + 1e-30):.2f} of the sum of magnitudes")
+    assert bool((off <= tol).all()), float((off / tol).max())
