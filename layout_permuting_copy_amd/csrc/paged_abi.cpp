@@ -92,7 +92,8 @@ void injective(const char* name, const Operand& o, int rank, int eb) {
 }
 
 // Whether two injective operands of one shape share no element: ranges apart, or the same strides
-// and a gap that lies between the spans of two neighbouring modes (halves of one allocation).
+// and a gap that is the stride of one more mode, of two, in an injective layout (halves of one allocation): it lies
+// between the spans of two neighbouring modes, and every larger stride exceeds both operands' span.
 bool disjoint(const Operand& x, const Operand& y, int rank, int eb) {
   if (!overlap(x.r, y.r)) return true;
   const Operand &a = x.r.lo < y.r.lo ? x : y, &b = x.r.lo < y.r.lo ? y : x;
@@ -108,13 +109,13 @@ bool disjoint(const Operand& x, const Operand& y, int rank, int eb) {
       order[at] = k;
     }
   const __int128 gap = b.r.lo - a.r.lo;
-  __int128 span = eb;
+  __int128 span = eb;  // of the modes order[0 .. i-1]
+  bool held = false;   // they lie inside the gap, or a smaller mode's do, and those since step over both operands
   for (int i = 0; i <= n; ++i) {
-    // modes order[0 .. i-1] lie inside the gap, order[i] steps over both operands' blocks
-    if (gap >= span && (i == n || gap + span <= a.s[order[i]])) return true;
+    held = (held || gap >= span) && (i == n || gap + span <= a.s[order[i]]);
     if (i < n) span += __int128(a.e[order[i]] - 1) * a.s[order[i]];
   }
-  return false;
+  return held;
 }
 
 void unit_inner(const char* name, const Operand& o, int k, int eb) {
