@@ -121,9 +121,13 @@ __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs
   if (tid < ROWS) {
     const uint32_t t = t0 + tid;
     int b = int(t), pos = -1, page = -1;
+    const auto length = [&](int of) {
+      const int n = a.lens[of];
+      return n < 0 ? 0 : n;
+    };
     if (t < uint32_t(a.tokens) && t <= udiv(row0 + ROWS - 1, heads)) {
       if (!a.starts) {
-        pos = a.lens[b] - 1;
+        pos = length(b) - 1;
       } else {
         // the last b with starts[b] <= t
         int lo = 0, hi = batch;
@@ -133,7 +137,7 @@ __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs
         }
         b = lo;
         const int first = listed ? starts[b] : a.starts[b], end = listed ? starts[b + 1] : a.starts[b + 1];
-        if (first <= int(t) && int(t) < end) pos = a.lens[b] - (end - int(t));
+        if (first <= int(t) && int(t) < end) pos = length(b) - (end - int(t));
       }
       if (pos >= 0) {
         const uint32_t col = udiv(uint32_t(pos), p.div);

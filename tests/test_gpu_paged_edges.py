@@ -133,3 +133,18 @@ def test_attention_weights_have_the_precision_of_fp32(kind, group):
     tol = 12 * R.STEP32 * mag + _half_step(dt, want, 12 * R.STEP32 * mag)
     say(f"[gpu] off by at most 2^{math.log2(float((off / mag).max()) + 1e-30):.2f} of the sum of magnitudes")
     assert bool((off <= tol).all()), float((off / tol).max())
+
+
+@pytest.mark.parametrize("length", [-(2 ** 31), -(2 ** 31) + 2, -1, 0])
+def test_append_to_a_sequence_of_negative_length_writes_nothing(length):
+    """Lengths are taken as at least 0, also where the table holds 2^31 rows and more."""
+    page = 1 << 20
+    k, v = (torch.full((1, page, 1, 16), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache = L.PagedCache(k, v)
+    table = torch.zeros(1, 2 ** 31 // page, dtype=torch.int32, device="cuda")
+    new = torch.ones(4, 1, 16, dtype=torch.bfloat16, device="cuda")
+    say(f"[gpu] append to length {length}")
+    L.tc_paged_append(cache, new[:1], new[:1], table, _i32([length]))
+    L.tc_paged_append(cache, new, new, table, _i32([length]), token_starts=_i32([0, 4]))
+    torch.cuda.synchronize()
+    assert bool((k == 5.0).all()) and bool((v == 5.0).all())
