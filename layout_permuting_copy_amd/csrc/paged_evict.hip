@@ -241,23 +241,34 @@ __global__ __launch_bounds__(kCopyThreads) void paged_move_kernel(EvictArgs a, D
   }
 }
 
+// Lanes a row of so many bytes takes, 16 bytes each, and the workgroups that the rows of one (sequence, head) take.
+constexpr int move_lanes(int row_bytes) {
+  int lanes = 1;
+  while (16 * lanes < row_bytes) lanes *= 2;
+  return lanes;
+}
+constexpr int64_t move_chunks(int most, int lanes) {
+  const int per = kCopyThreads / lanes * kCopyRounds;
+  return (int64_t(most) + per - 1) / per;
+}
+
 template <bool E4M3, int LPR>
 void move(const EvictArgs& a, int most, hipStream_t s) {
-  constexpr int per = kCopyThreads / LPR * kCopyRounds;
-  const int64_t chunks = (int64_t(most) + per - 1) / per, wgs = chunks * a.table.batch * a.heads;
+  const int64_t chunks = move_chunks(most, LPR), wgs = chunks * a.table.batch * a.heads;
   hipLaunchKernelGGL((paged_move_kernel<E4M3, LPR>), dim3(uint32_t(wgs)), dim3(kCopyThreads), 0, s, a,
                      make_div32(uint32_t(a.heads)), make_div32(uint32_t(chunks)));
 }
 
 template <bool E4M3>
 void move_rows(const EvictArgs& a, int most, hipStream_t s) {
-  const int lanes = a.row_bytes / 16;
-  if (lanes <= 1) return move<E4M3, 1>(a, most, s);
-  if (lanes <= 2) return move<E4M3, 2>(a, most, s);
-  if (lanes <= 4) return move<E4M3, 4>(a, most, s);
-  if (lanes <= 8) return move<E4M3, 8>(a, most, s);
-  if (lanes <= 16) return move<E4M3, 16>(a, most, s);
-  return move<E4M3, 32>(a, most, s);
+  switch (move_lanes(a.row_bytes)) {
+    case 1: return move<E4M3, 1>(a, most, s);
+    case 2: return move<E4M3, 2>(a, most, s);
+    case 4: return move<E4M3, 4>(a, most, s);
+    case 8: return move<E4M3, 8>(a, most, s);
+    case 16: return move<E4M3, 16>(a, most, s);
+    default: return move<E4M3, 32>(a, most, s);
+  }
 }
 
 }  // namespace dev
@@ -265,9 +276,9 @@ void move_rows(const EvictArgs& a, int most, hipStream_t s) {
 int launch_paged_evict(const EvictArgs& a, int cache_dtype, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int most = a.budget < a.max_len ? a.budget : a.max_len;
-  // both grids have to fit before anything is launched (the move's: 8 rows a workgroup at the widest rows)
-  const int64_t rows = int64_t(a.table.batch) * a.heads;
-  if (!launchable(rows, 1024) || !launchable((int64_t(most) / 8 + 1) * rows, dev::kCopyThreads)) return TC_E_RANGE;
+  // both grids have to fit before anything is launched
+  const int64_t rows = int64_t(a.table.batch) * a.heads, chunks = dev::move_chunks(most, dev::move_lanes(a.row_bytes));
+  if (!launchable(rows, 1024) || !launchable(chunks * rows, dev::kCopyThreads)) return TC_E_RANGE;
   if (a.max_len <= 1024)
     dev::select<256, 4, 1>(a, s);
   else if (a.max_len <= 4096)

@@ -2,9 +2,10 @@
 device addresses are never dereferenced."""
 
 import pytest
+import torch
 
 import layout_permuting_copy_amd as L
-from test_paged_refusals import BASE, DIM, HEADS, PAGE, PAGES, _append, _cache
+from test_paged_refusals import BASE, DIM, HEADS, PAGE, PAGES, _append, _cache, _evict
 
 
 def _named(shape, stride, base):
@@ -60,3 +61,23 @@ def test_scales_that_share_rows_are_refused():
         c = _cache(dtype=L.TC_E4M3, ks=BASE + (25 << 20), vs=BASE + (25 << 20) + 4 * HEADS)
         c.k_scale_layout = c.v_scale_layout = L.make_layout((PAGES, PAGE, HEADS), (page, 2 * HEADS, 1))
         assert _append(c, new=(3, HEADS, 80)) == want, L.tc_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that passes the checks would be launched on made-up addresses")
+@pytest.mark.parametrize("dtype, dim, rows_a_workgroup", [
+    (L.TC_BF16, 16, 128), (L.TC_BF16, 64, 32), (L.TC_BF16, 80, 16), (L.TC_BF16, 128, 16), (L.TC_BF16, 256, 8),
+    (L.TC_E4M3, 16, 256), (L.TC_E4M3, 128, 32), (L.TC_E4M3, 144, 16), (L.TC_E4M3, 256, 16)])
+def test_eviction_is_refused_only_past_its_own_grid(dtype, dim, rows_a_workgroup):
+    """The copy takes 256 lanes for 4096 bytes of rows of a power of two: calls of just under 2^32 lanes go on to the launch
+    (which finds no GPU here), calls of 2^32 are refused."""
+    batch = 2048
+    chunks = 2 ** 32 // 256 // (batch * HEADS)  # workgroups a sequence and head that make 2^32 lanes
+    for most, want in (((chunks - 1) * rows_a_workgroup, L.TC_E_HIP), ((chunks - 1) * rows_a_workgroup + 1, L.TC_E_RANGE),
+                       (chunks * rows_a_workgroup, L.TC_E_RANGE)):
+        shape, at = (PAGES, 1 << 20, HEADS, dim), 1 << 40
+        scales = [None] * 4 if dtype == L.TC_BF16 else [(40 + i) * at for i in range(4)]
+        src = _cache(dtype, 1 * at, 2 * at, shape, ks=scales[0], vs=scales[1])
+        dst = _cache(dtype, 3 * at, 4 * at, shape, ks=scales[2], vs=scales[3])
+        rc = _evict(src, dst, table=(batch, 1), dst_table=(batch, 1), budget=most, recent=0, max_len=most, w=5 * at,
+                    w_shape=(batch, HEADS, most), kept=6 * at, kept_shape=(batch, HEADS, most), lens_out=7 * at, lens=8 * at)
+        assert rc == want, (most, rc, L.tc_last_error())
