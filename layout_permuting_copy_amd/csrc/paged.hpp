@@ -94,7 +94,7 @@ struct EvictArgs {
   PagedRows kr;
   float* weights_out;  // or NULL
   PagedRows wo;
-  int32_t heads, head_dim, row_bytes;
+  int32_t heads, row_bytes;
   int32_t max_len, budget, recent;
 };
 

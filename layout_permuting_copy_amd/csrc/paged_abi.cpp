@@ -509,7 +509,6 @@ int tc_paged_evict(const tc_paged_cache* src, const int32_t* block_table, const 
     a.kept = reinterpret_cast<int32_t*>(kp.p);
     a.weights_out = wo.empty ? nullptr : reinterpret_cast<float*>(wo.p);
     a.heads = int32_t(s.heads);
-    a.head_dim = int32_t(s.dim);
     a.row_bytes = int32_t(s.dim * s.eb);
     a.max_len = int32_t(max_len);
     a.budget = int32_t(budget);

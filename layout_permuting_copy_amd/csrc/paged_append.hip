@@ -4,10 +4,7 @@
 namespace tc {
 namespace dev {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRounds = 1;     // rows a lane moves (1, 2, 4: the prompts in 27, 29, 31 us)
 constexpr int kAppendStarts = 2048;  // token_starts kept in LDS
 
 // Eight 2-byte values at p: one 16-byte load, or element loads where rows are not 16-byte aligned.
@@ -80,34 +77,26 @@ __device__ __forceinline__ void store_row(const u32x4& v, int c, bool active, un
   }
 }
 
-// A workgroup moves kAppendThreads / LPR * kAppendRounds (token, head) rows; LPR lanes a row, of which head_dim / 8
-// move eight values each of the key and of the value.  The rows are on their way while the place of each of the
-// workgroup's tokens is found, once for all its heads: its sequence by a binary search of token_starts (in LDS
-// where they fit), then length, page, offset.
+// A workgroup moves kAppendThreads / LPR (token, head) rows; LPR lanes a row, of which head_dim / 8
+// move eight values each of the key and of the value (one row a lane: the prompts in 27 us, two 29, four 31).  The rows are
+// on their way while the place of each of the workgroup's tokens is found, once for all its heads: its sequence by a
+// binary search of token_starts (in LDS where they fit), then length, page, offset.
 // Bound: HBM for prompts (16665 tokens of 8 heads of 128: 137 MB in 26.0 us, 5.3 TB/s; new rows are read and cache rows
 // written past the caches), the latency of starts -> length -> table -> row otherwise (32 single tokens 2.7 us, 6994
 // tokens of 8 heads of 64 to 8 bits 8.5 us).
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
 __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs a, Div32 heads) {
-  constexpr int RPR = kAppendThreads / LPR;         // rows a round
-  constexpr int ROWS = RPR * kAppendRounds;
+  constexpr int ROWS = kAppendThreads / LPR;
   __shared__ int starts[kAppendStarts];
   __shared__ int place_seq[ROWS], place_page[ROWS], place_pos[ROWS];  // page -1: nowhere
   const int tid = threadIdx.x, c = tid % LPR;
   const uint32_t row0 = blockIdx.x * ROWS, t0 = udiv(row0, heads);  // rows count heads within tokens
-  u32x4 k[kAppendRounds], v[kAppendRounds];
-  uint32_t token[kAppendRounds];
-  int head[kAppendRounds];
-#pragma unroll
-  for (int i = 0; i < kAppendRounds; ++i) {
-    const uint32_t row = row0 + i * RPR + tid / LPR;
-    token[i] = udiv(row, heads);
-    head[i] = int(row - token[i] * heads.d);
-    k[i] = v[i] = u32x4{};
-    if (token[i] < uint32_t(a.tokens) && 8 * c < a.head_dim) {
-      k[i] = load8<WIDE>(a.k + int64_t(token[i]) * a.kt + head[i] * a.kh + 16 * c);
-      v[i] = load8<WIDE>(a.v + int64_t(token[i]) * a.vt + head[i] * a.vh + 16 * c);
-    }
+  const uint32_t row = row0 + tid / LPR, token = udiv(row, heads);
+  const int h = int(row - token * heads.d);
+  u32x4 k{}, v{};
+  if (token < uint32_t(a.tokens) && 8 * c < a.head_dim) {
+    k = load8<WIDE>(a.k + int64_t(token) * a.kt + h * a.kh + 16 * c);
+    v = load8<WIDE>(a.v + int64_t(token) * a.vt + h * a.vh + 16 * c);
   }
   const PagedPool& p = a.pool;
   const int batch = a.table.batch;
@@ -149,32 +138,28 @@ __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs
     place_pos[tid] = pos;
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kAppendRounds; ++i) {
-    const int at = int(token[i] - t0), b = place_seq[at], page = place_page[at], pos = place_pos[at];
-    const bool out = page >= 0 && 8 * c < a.head_dim;
-    const int h = head[i];
-    unsigned char* kd = nullptr;
-    unsigned char* vd = nullptr;
-    float *ks = nullptr, *vs = nullptr;
-    if (out) {
-      const uint32_t r = uint32_t(pos) - udiv(uint32_t(pos), p.div) * p.div.d;
-      kd = p.k + page * p.kp + r * p.kr + h * p.kh;
-      vd = p.v + page * p.vp + r * p.vr + h * p.vh;
-      if constexpr (E4M3) {
-        ks = p.ks + page * p.ksp + r * p.ksr + h * p.ksh;
-        vs = p.vs + page * p.vsp + r * p.vsr + h * p.vsh;
-      }
-      if (a.weights && c == 0 && pos < a.w.cols) a.weights[b * a.w.sb + h * a.w.sh + pos * a.w.sc] = 0.0f;
+  const int at = int(token - t0), b = place_seq[at], page = place_page[at], pos = place_pos[at];
+  const bool out = page >= 0 && 8 * c < a.head_dim;
+  unsigned char* kd = nullptr;
+  unsigned char* vd = nullptr;
+  float *ks = nullptr, *vs = nullptr;
+  if (out) {
+    const uint32_t r = uint32_t(pos) - udiv(uint32_t(pos), p.div) * p.div.d;
+    kd = p.k + page * p.kp + r * p.kr + h * p.kh;
+    vd = p.v + page * p.vp + r * p.vr + h * p.vh;
+    if constexpr (E4M3) {
+      ks = p.ks + page * p.ksp + r * p.ksr + h * p.ksh;
+      vs = p.vs + page * p.vsp + r * p.vsr + h * p.vsh;
     }
-    store_row<BF16, E4M3, LPR>(k[i], c, out, kd, ks);
-    store_row<BF16, E4M3, LPR>(v[i], c, out, vd, vs);
+    if (a.weights && c == 0 && pos < a.w.cols) a.weights[b * a.w.sb + h * a.w.sh + pos * a.w.sc] = 0.0f;
   }
+  store_row<BF16, E4M3, LPR>(k, c, out, kd, ks);
+  store_row<BF16, E4M3, LPR>(v, c, out, vd, vs);
 }
 
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
 int launch(const AppendArgs& a, hipStream_t s) {
-  const int64_t per = kAppendThreads / LPR * kAppendRounds;
+  const int64_t per = kAppendThreads / LPR;
   const int64_t wgs = (a.tokens * a.heads + per - 1) / per;
   if (!launchable(wgs, kAppendThreads)) return TC_E_RANGE;
   hipLaunchKernelGGL((paged_append_kernel<BF16, E4M3, WIDE, LPR>), dim3(uint32_t(wgs)), dim3(kAppendThreads), 0, s, a,

@@ -190,54 +190,43 @@ void select(const EvictArgs& a, hipStream_t s) {
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyRounds = 1;  // rows a lane moves (1, 2, 4: level)
 
-// The kept rows of keys and values into their new pages: LPR lanes a row, 16 bytes a lane, kCopyRounds rows
-// on their way at once.  Grid: (sequence, rows, head), the heads fastest: those of the same new rows are neighbours
+// The kept rows of keys and values into their new pages: LPR lanes a row, 16 bytes a lane (two or four
+// rows a lane: level).  Grid: (sequence, rows, head), the heads fastest: those of the same new rows are neighbours
 // where a pool keeps a row's heads together.  Bound: HBM, by rows of 256 bytes read here and there (16 sequences to
 // 4096 rows: 408 MB in 84 us, 4.9 TB/s).
 template <bool E4M3, int LPR>
 __global__ __launch_bounds__(kCopyThreads) void paged_move_kernel(EvictArgs a, Div32 heads, Div32 chunks) {
-  constexpr int RPR = kCopyThreads / LPR;
+  constexpr int ROWS = kCopyThreads / LPR;
   const uint32_t bc = udiv(blockIdx.x, heads), bb = udiv(bc, chunks), chunk = bc - bb * chunks.d;
   const int b = int(bb), h = int(blockIdx.x - bc * heads.d);
   const int n = paged_len(a.lens, b, a.max_len);
   const int kept_n = n < a.budget ? n : a.budget;
-  const int j0 = int(chunk) * RPR * kCopyRounds + int(threadIdx.x) / LPR, c = threadIdx.x % LPR;
-  if (int(chunk) * RPR * kCopyRounds >= kept_n) return;
+  const int j = int(chunk) * ROWS + int(threadIdx.x) / LPR, c = threadIdx.x % LPR;
+  if (int(chunk) * ROWS >= kept_n) return;
   const int32_t* kept = a.kept + b * a.kr.sb + h * a.kr.sh;
-  int from[kCopyRounds], sp[kCopyRounds], dp[kCopyRounds];
-#pragma unroll
-  for (int r = 0; r < kCopyRounds; ++r) {
-    const int j = j0 + r * RPR;
-    from[r] = kept[(j < kept_n ? j : 0) * a.kr.sc];
-    dp[r] = j < kept_n ? paged_page(a.dst_table, a.dst, b, udiv(uint32_t(j), a.dst.div)) : -1;
-  }
-  u32x4 k[kCopyRounds], v[kCopyRounds];
-  float ks[kCopyRounds], vs[kCopyRounds];
-#pragma unroll
-  for (int r = 0; r < kCopyRounds; ++r) sp[r] = paged_page(a.table, a.src, b, udiv(uint32_t(from[r]), a.src.div));
-#pragma unroll
-  for (int r = 0; r < kCopyRounds; ++r) {
-    if (sp[r] < 0 || dp[r] < 0 || 16 * c >= a.row_bytes) continue;
-    const uint32_t row = uint32_t(from[r]) - udiv(uint32_t(from[r]), a.src.div) * a.src.div.d;
-    gload<16, 1>(a.src.k + sp[r] * a.src.kp + row * a.src.kr + h * a.src.kh + 16 * c, reinterpret_cast<uint32_t*>(&k[r]));
-    gload<16, 1>(a.src.v + sp[r] * a.src.vp + row * a.src.vr + h * a.src.vh + 16 * c, reinterpret_cast<uint32_t*>(&v[r]));
+  const int from = kept[(j < kept_n ? j : 0) * a.kr.sc];
+  const int dp = j < kept_n ? paged_page(a.dst_table, a.dst, b, udiv(uint32_t(j), a.dst.div)) : -1;
+  const int sp = paged_page(a.table, a.src, b, udiv(uint32_t(from), a.src.div));
+  const bool moves = sp >= 0 && dp >= 0 && 16 * c < a.row_bytes;
+  const uint32_t src_row = uint32_t(from) - udiv(uint32_t(from), a.src.div) * a.src.div.d;
+  const uint32_t dst_row = uint32_t(j) - udiv(uint32_t(j), a.dst.div) * a.dst.div.d;
+  u32x4 k, v;
+  float ks, vs;
+  if (moves) {
+    gload<16, 1>(a.src.k + sp * a.src.kp + src_row * a.src.kr + h * a.src.kh + 16 * c, reinterpret_cast<uint32_t*>(&k));
+    gload<16, 1>(a.src.v + sp * a.src.vp + src_row * a.src.vr + h * a.src.vh + 16 * c, reinterpret_cast<uint32_t*>(&v));
     if (E4M3 && c == 0) {
-      ks[r] = a.src.ks[sp[r] * a.src.ksp + row * a.src.ksr + h * a.src.ksh];
-      vs[r] = a.src.vs[sp[r] * a.src.vsp + row * a.src.vsr + h * a.src.vsh];
+      ks = a.src.ks[sp * a.src.ksp + src_row * a.src.ksr + h * a.src.ksh];
+      vs = a.src.vs[sp * a.src.vsp + src_row * a.src.vsr + h * a.src.vsh];
     }
   }
-#pragma unroll
-  for (int r = 0; r < kCopyRounds; ++r) {
-    if (sp[r] < 0 || dp[r] < 0 || 16 * c >= a.row_bytes) continue;
-    const uint32_t j = uint32_t(j0 + r * RPR), row = j - udiv(j, a.dst.div) * a.dst.div.d;
-    gstore<16, 2>(a.dst.k + dp[r] * a.dst.kp + row * a.dst.kr + h * a.dst.kh + 16 * c, reinterpret_cast<uint32_t*>(&k[r]));
-    gstore<16, 2>(a.dst.v + dp[r] * a.dst.vp + row * a.dst.vr + h * a.dst.vh + 16 * c, reinterpret_cast<uint32_t*>(&v[r]));
-    if (E4M3 && c == 0) {
-      a.dst.ks[dp[r] * a.dst.ksp + row * a.dst.ksr + h * a.dst.ksh] = ks[r];
-      a.dst.vs[dp[r] * a.dst.vsp + row * a.dst.vsr + h * a.dst.vsh] = vs[r];
-    }
+  if (!moves) return;
+  gstore<16, 2>(a.dst.k + dp * a.dst.kp + dst_row * a.dst.kr + h * a.dst.kh + 16 * c, reinterpret_cast<uint32_t*>(&k));
+  gstore<16, 2>(a.dst.v + dp * a.dst.vp + dst_row * a.dst.vr + h * a.dst.vh + 16 * c, reinterpret_cast<uint32_t*>(&v));
+  if (E4M3 && c == 0) {
+    a.dst.ks[dp * a.dst.ksp + dst_row * a.dst.ksr + h * a.dst.ksh] = ks;
+    a.dst.vs[dp * a.dst.vsp + dst_row * a.dst.vsr + h * a.dst.vsh] = vs;
   }
 }
 
@@ -248,7 +237,7 @@ constexpr int move_lanes(int row_bytes) {
   return lanes;
 }
 constexpr int64_t move_chunks(int most, int lanes) {
-  const int per = kCopyThreads / lanes * kCopyRounds;
+  const int per = kCopyThreads / lanes;
   return (int64_t(most) + per - 1) / per;
 }
 
@@ -261,14 +250,16 @@ void move(const EvictArgs& a, int most, hipStream_t s) {
 
 template <bool E4M3>
 void move_rows(const EvictArgs& a, int most, hipStream_t s) {
-  switch (move_lanes(a.row_bytes)) {
-    case 1: return move<E4M3, 1>(a, most, s);
-    case 2: return move<E4M3, 2>(a, most, s);
-    case 4: return move<E4M3, 4>(a, most, s);
-    case 8: return move<E4M3, 8>(a, most, s);
-    case 16: return move<E4M3, 16>(a, most, s);
-    default: return move<E4M3, 32>(a, most, s);
+  const int lanes = move_lanes(a.row_bytes);
+  if constexpr (E4M3) {
+    if (lanes == 1) return move<E4M3, 1>(a, most, s);
+  } else {
+    if (lanes == 32) return move<E4M3, 32>(a, most, s);
   }
+  if (lanes == 2) return move<E4M3, 2>(a, most, s);
+  if (lanes == 4) return move<E4M3, 4>(a, most, s);
+  if (lanes == 8) return move<E4M3, 8>(a, most, s);
+  return move<E4M3, 16>(a, most, s);
 }
 
 }  // namespace dev
