@@ -409,7 +409,7 @@ int tc_paged_append(const tc_paged_cache* cache, const void* k_new, const tc_lay
  * heads, capacity >= max_len), fp32, may be NULL: receives weights[b][h][i] + the sum of p_i over the head's group,
  * for i < n; weights (the same shape) may be weights_out itself (sums grow in place) or not overlap it; rows from n on
  * are left as they are.
- * workspace: tc_paged_attention_workspace(...) bytes of device memory, 16-byte aligned, used until
+ * workspace: tc_paged_attention_workspace(...) bytes of device memory (a call may use fewer), 16-byte aligned, used until
  * the call's kernels end and by no other call meanwhile; may be NULL where that is 0.
  * Errors: as above, TC_E_RANGE (q_heads above 65535, sizes the kernels or a launch cannot count); TC_E_ARG (workspace
  * too small, bad scale), TC_E_ALIAS (an output overlaps an input).
@@ -421,8 +421,9 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
                        const tc_layout* weights_layout, float* weights_out, const tc_layout* weights_out_layout,
                        void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that tc_paged_attention needs for these sizes (0: none), or a negative status.
- * Host only. */
+/* Bytes of workspace that suffice for tc_paged_attention at these sizes and at any smaller batch and max_len (0: none is
+ * needed), or a negative status.  With weights that holds batch * q_heads * max_len floats: a tight max_len keeps it
+ * small.  Host only. */
 int64_t tc_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim,
                                      int64_t max_len, int with_weights);
 

@@ -100,12 +100,13 @@ struct EvictArgs {
 
 // How an attention call is cut over the cache's length: units of `unit_rows` rows (at most `units` in all), `runs` runs
 // of at least least_units of them, query heads in tiles of tile_heads, at most `workgroups` workgroups; whether a
-// sequence's rows can fall to more than one run.
+// sequence's rows can fall to more than one run.  `most`: as a call of a smaller batch may be cut where this one is not, so
+// that sizes that follow from it grow with batch and max_len.
 struct PagedCut {
   int64_t unit_rows, units, least_units, runs, workgroups, tile_heads, head_tiles;
   bool cuts;
 };
-PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
+PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len, bool most);
 // Columns a row of the logits workspace holds: max_len rounded up to whole tiles.
 int64_t paged_logit_row(int64_t max_len);
 

@@ -276,10 +276,11 @@ struct Workspace {
   int64_t o, ml, parts, final_ml, logits;
   int64_t bytes() const { return 4 * (o + ml + parts + final_ml + logits); }
 };
-Workspace workspace_of(int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_len, bool weights) {
+Workspace workspace_of(int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_len, bool weights,
+                       bool most) {
   Workspace w{};
   if (batch == 0 || q_heads == 0) return w;
-  w.cut = tc::paged_cut(batch, heads, q_heads / heads, head_dim, max_len);
+  w.cut = tc::paged_cut(batch, heads, q_heads / heads, head_dim, max_len, most);
   need(w.cut.units < (int64_t(1) << 31) && w.cut.workgroups < (int64_t(1) << 31) && __int128(batch) * q_heads * max_len < kLim, TC_E_RANGE,
        "batch, heads and max_len beyond what the kernels count");
   if (w.cut.cuts) {
@@ -348,7 +349,7 @@ int64_t tc_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t hea
   int64_t bytes = 0;
   const int rc = guarded([&]() -> int {
     attention_sizes(batch, q_heads, heads, head_dim, max_len);
-    bytes = workspace_of(batch, q_heads, heads, head_dim, max_len, with_weights != 0).bytes();
+    bytes = workspace_of(batch, q_heads, heads, head_dim, max_len, with_weights != 0, true).bytes();
     return TC_OK;
   });
   return rc == TC_OK ? bytes : rc;
@@ -397,7 +398,7 @@ int tc_paged_attention(const tc_paged_cache* cache, const void* q, const tc_layo
     unit_inner("out", oo, 2, eb);
     injective("out", oo, 3, eb);
     const bool with_weights = weights_out != nullptr && max_len > 0;
-    const Workspace ws = workspace_of(batch, q_heads, c.heads, c.dim, max_len, with_weights);
+    const Workspace ws = workspace_of(batch, q_heads, c.heads, c.dim, max_len, with_weights, false);
     need(workspace_bytes >= ws.bytes(), TC_E_ARG, "workspace too small");
     need(workspace || ws.bytes() == 0, TC_E_NULL, "null workspace");
     need(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, TC_E_ALIGN, "workspace not aligned to 16 bytes");

@@ -857,7 +857,7 @@ static int64_t runs_of(int64_t units, int64_t least, int64_t pairs, int64_t resi
   return std::min((units + least - 1) / least, fit);
 }
 
-PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len) {
+PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len, bool most) {
   PagedCut c{};
   // 32 heads at once for larger groups, where their outputs fit the registers
   c.tile_heads = group > 16 && head_dim <= 128 ? 32 : 16;
@@ -871,7 +871,7 @@ PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim
   // in 9 us uncut, 513 in 12 us cut), and eight turns where every CU has a sequence and head anyway (8 heads of 128,
   // mixed lengths, uncut and cut: 16 sequences of up to 1000 rows 17 and 16 us, 32 18 and 23, 512 171 and 188; of up
   // to 2000 rows 32 sequences 31 and 30, 64 58 and 53)
-  if (max_len <= 512 || (max_len <= 1024 && batch * pairs >= dev::kCus)) {
+  if (max_len <= 512 || (max_len <= 1024 && batch * pairs >= dev::kCus && !most)) {
     c.unit_rows = std::max<int64_t>(dev::kStep, (max_len + dev::kStep - 1) / dev::kStep * dev::kStep);
     c.least_units = 1;
   }

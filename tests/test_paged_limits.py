@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import layout_permuting_copy_amd as L
-from test_paged_refusals import BASE, DIM, HEADS, PAGE, PAGES, _append, _cache, _evict
+from test_paged_refusals import BASE, DIM, HEADS, PAGE, PAGES, _append, _attend, _cache, _evict
 
 
 def _named(shape, stride, base):
@@ -81,3 +81,29 @@ def test_eviction_is_refused_only_past_its_own_grid(dtype, dim, rows_a_workgroup
         rc = _evict(src, dst, table=(batch, 1), dst_table=(batch, 1), budget=most, recent=0, max_len=most, w=5 * at,
                     w_shape=(batch, HEADS, most), kept=6 * at, kept_shape=(batch, HEADS, most), lens_out=7 * at, lens=8 * at)
         assert rc == want, (most, rc, L.tc_last_error())
+
+
+@pytest.mark.parametrize("q_heads, heads, dim", [(32, 8, 128), (1, 1, 64), (40, 2, 96), (20, 1, 256), (48, 48, 64)])
+@pytest.mark.parametrize("weights", [0, 1])
+def test_a_workspace_suffices_for_smaller_calls(q_heads, heads, dim, weights):
+    """The workspace of a batch and max_len is enough for every smaller one, as a serving loop or graphs of several batch
+    sizes allocate it once; a call that is given it gets past the check of its size."""
+    size = L.load_library().tc_paged_attention_workspace
+    batches, lengths = (1, 2, 7, 8, 16, 31, 32, 33, 64, 255, 256, 257, 1000), (1, 128, 511, 512, 513, 1000, 1024, 1025, 2048, 20000)
+    grid = [[size(b, q_heads, heads, dim, n, weights) for n in lengths] for b in batches]
+    assert min(map(min, grid)) >= 0
+    for row in grid:
+        assert row == sorted(row), (row, lengths)
+    for column in zip(*grid):
+        assert list(column) == sorted(column), (column, batches)
+    cache = _cache(shape=(PAGES, PAGE, heads, dim), k=1 << 40, v=1 << 41)
+    at = 1 << 42
+    for b in batches:
+        for n in lengths:  # out overlaps q: refused, but later than a small workspace is
+            rc = _attend(cache, q=at, out=at, q_shape=(b, q_heads, dim), table=(b, 4), max_len=n, work=1 << 43, work_bytes=grid[-1][-1],
+                         lens=1 << 44, w=1 << 45 if weights else None, wo=1 << 45 if weights else None, w_shape=(b, heads, n))
+            assert rc == L.TC_E_ALIAS, (b, n, L.tc_last_error())
+            rc = _attend(cache, q=at, out=at, q_shape=(b, q_heads, dim), table=(b, 4), max_len=n, work=1 << 43,
+                         work_bytes=size(b, q_heads, heads, dim, n, weights), lens=1 << 44, w=1 << 45 if weights else None,
+                         wo=1 << 45 if weights else None, w_shape=(b, heads, n))
+            assert rc == L.TC_E_ALIAS, (b, n, L.tc_last_error())
