@@ -148,3 +148,75 @@ def test_append_to_a_sequence_of_negative_length_writes_nothing(length):
     L.tc_paged_append(cache, new, new, table, _i32([length]), token_starts=_i32([0, 4]))
     torch.cuda.synchronize()
     assert bool((k == 5.0).all()) and bool((v == 5.0).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [1, 100, 5000])
+@pytest.mark.parametrize("least", [0.25, 1.0])
+def test_attention_beside_rows_of_the_lowest_value(kind, rows, least):
+    """Two rows of three have the type's lowest key (or a quarter of it) and weigh nothing; the others are as exact as if
+    they were alone.  With e = 2^-24: a logit x (one key element, so without a sum) is off by e |x| for each of scale and product, and
+    by e for the difference to the maximum; a weight by twice that and 16 e for its exponential, the parts' factors and the
+    division; a sum over rows is formed in n / 16 + 96 additions."""
+    dt, dim, group = R.DT[kind], 64, 5
+    gen = torch.Generator().manual_seed(rows)
+    live = torch.arange(rows) % 3 == 0
+    x = torch.randn(rows, generator=gen).to(dt)
+    k = torch.zeros(rows, dim, dtype=dt)
+    k[:, 0] = torch.where(live, x, torch.full((rows,), torch.finfo(dt).min).to(dt) * least)
+    v = torch.randn(rows, dim, generator=gen).to(dt)
+    v[~live] *= 64.0
+    q = torch.zeros(group, dim, dtype=dt)
+    q[:, 0] = 1.0 / 8.0  # (the lowest bf16 times log2 e would leave fp32's range)
+    xs = x[live].double()
+    p = torch.softmax(xs, 0)
+    want, mag = p @ v[live].double(), p @ v[live].double().abs()
+    dx = (3 * float(xs.abs().max()) + 1) * R.STEP32
+    rel = 2 * dx + 16 * R.STEP32 + (rows / 16 + 96) * R.STEP32
+    assert rel < 2.0 ** -14
+    say(f"[gpu] {kind}, {rows} rows, lowest keys times {least}")
+    lse, w = torch.zeros(1, group, device="cuda"), torch.zeros(1, 1, rows, device="cuda")
+    out = L.tc_paged_attention(*_one_sequence(k, v, q), scale=8.0, max_len=rows, lse=lse, weights=w)
+    assert bool(((out[0].cpu().double() - want).abs() <= rel * mag + _half_step(dt, want, rel * mag)).all())
+    total = torch.logsumexp(xs, 0)
+    assert bool(((lse.cpu().double() - total).abs() <= rel + 4 * R.STEP32 * (abs(total) + xs.abs().max())).all())
+    weight = torch.zeros(rows, dtype=torch.float64)
+    weight[live] = group * p
+    assert bool(((w[0, 0].cpu().double() - weight).abs() <= (rel + group * R.STEP32) * weight).all())
+
+
+def test_weights_and_sums_of_calls_from_threads():
+    """Threads on streams of their own that add weights up: weights, log-sums and outputs of every call are as alone."""
+    import threading
+    jobs, errors = [], []
+    for i in range(6):
+        gen = torch.Generator().manual_seed(190 + i)
+        lens = [70 * i + 1, 1900 - 300 * i, 17]
+        kind = ("bf16", "fp16", "e4m3")[i % 3]
+        table, pages = R.table_for(lens, 16, gen)
+        pool = R.Pool(kind, pages, 16, 2, 64, "rows", gen)
+        q = torch.randn(3, 8, 64, generator=gen).to(torch.float16 if kind == "fp16" else torch.bfloat16)
+        jobs.append((pool.on_gpu(), q.cuda(), table.cuda(), _i32(lens), max(lens), R.attention(q, pool, table, lens, 16)))
+    torch.cuda.synchronize()
+
+    def work(cache, q, table, lens, most, ref):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(8):
+                    w, lse = torch.zeros(3, 2, most, device="cuda"), torch.zeros(3, 8, device="cuda")
+                    out = L.tc_paged_attention(q, cache, table, lens, weights=w, lse=lse, max_len=most)
+                    s.synchronize()
+                    for got, want, tol in ((w, ref[2], ref[5] + 2 * R.STEP32 * ref[2]), (lse, ref[1], ref[4]),
+                                           (out, ref[0], ref[3] + _half_step(q.dtype, ref[0], ref[3]))):
+                        assert bool(((got.cpu().double() - want).abs() <= tol).all())
+        except BaseException as e:  # reported below
+            errors.append(repr(e))
+
+    say(f"[gpu] {len(jobs)} threads with weights")
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[:2]
