@@ -381,13 +381,14 @@ __device__ __forceinline__ const AttentionArgs& arguments_again() {
 
 constexpr int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 // Workgroups a CU gets at once, and the registers they are compiled for.  Fewer, longer runs cut fewer sequences and come
-// out more even, as long as they keep the memory busy: one workgroup's four waves do with 16-bit rows of 128 elements
-// and more (64 KB on their way; 64 sequences of mixed lengths: 88 us with one a CU, 93 with two or three), narrower
-// rows want two (8-bit rows of 128: 200 us with one, 187 with two, 194 with three).  Without FULL and PAGE 16
-// some more registers are needed.
+// out more even, as long as they keep the memory busy: one workgroup's four waves do with rows of 256 bytes and more
+// (64 KB on their way; 64 sequences of mixed lengths in 16-bit rows of 128: 88 us with one a CU, 93 with two or three; 8
+// of 16384 8-bit rows of 256: 99 with one, 101 with two, in pages of 24 107 and 110), narrower rows want two (8-bit rows of
+// 128: 200 us with one, 187 with two, 194 with three).  Two tiles of heads without FULL and PAGE 16 need more
+// registers than two workgroups have.
 constexpr int resident_workgroups(int dp, bool e4m3, int head_tiles, bool plain) {
   const int bytes = dp * (e4m3 ? 1 : 2);
-  return bytes >= 256 ? (dp == 256 && e4m3 && plain ? 2 : 1) : head_tiles == 1 || plain ? 2 : 1;
+  return bytes < 256 && (head_tiles == 1 || plain) ? 2 : 1;
 }
 
 template <bool BF16, bool E4M3, int DP, int HT, int PAGE, bool FULL>
