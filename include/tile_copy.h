@@ -402,9 +402,11 @@ int tc_paged_append(const tc_paged_cache* cache, const void* k_new, const tc_lay
  *   x_i = scale * q . k_i     lse = log sum_i exp x_i     p_i = exp(x_i - lse)     out = sum_i p_i v_i
  *
  * Sums, maxima and products accumulate in fp32, out is rounded once.  No row, or none with x_i above
- * -infinity: out = 0, lse = -infinity.  An infinite value under a weight makes its element of out NaN (values
- * are multiplied by weights held in parts).  Equal calls give equal bits; where a sequence's rows are cut
- * between workgroups, and with it the last bits of its sums, depends on the whole batch and max_len.  Rows past n and
+ * -infinity: out = 0, lse = -infinity.  The sum over rows is formed before its division: an element of out whose sum of
+ * exp(x_i - max x) |v_i| passes fp32's range is infinite or NaN (values near 3e38, of bf16 and of scaled 8-bit rows).
+ * An infinite value under a weight makes its element of out NaN (values are multiplied by weights held in parts).  Equal
+ * calls give equal bits; where a sequence's rows are cut between workgroups, and with it the last bits of its sums,
+ * depends on the whole batch and max_len.  Rows past n and
  * rows on no page are never used, whatever they hold.  lse (batch, q_heads), fp32, may be NULL.  weights_out (batch,
  * heads, capacity >= max_len), fp32, may be NULL: receives weights[b][h][i] + the sum of p_i over the head's group,
  * for i < n; weights (the same shape) may be weights_out itself (sums grow in place) or not overlap it; rows from n on

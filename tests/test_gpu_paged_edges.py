@@ -220,3 +220,19 @@ def test_weights_and_sums_of_calls_from_threads():
     for t in threads:
         t.join()
     assert not errors, errors[:2]
+
+
+@pytest.mark.parametrize("kind, values", [("bf16", (2.0 ** -133, 2.0 ** -127, 1e-37, 1e-30, 1.5e38)),
+                                          ("fp16", (2.0 ** -24, 3 * 2.0 ** -24, 2.0 ** -14, 65504.0))])
+def test_attention_over_values_at_the_ends_of_their_range(kind, values):
+    """Equal values under equal weights: out is the value, of subnormal numbers too, as long as the sum of the values times
+    exp(x_i - max x), here their number, stays in fp32's range."""
+    dt = R.DT[kind]
+    for value in values:
+        for rows in (1, 2, 40, 2000):
+            if value * rows > 3.4e38:
+                continue
+            say(f"[gpu] {rows} rows of {value} in {kind}")
+            v = torch.full((rows, 32), value).to(dt)
+            out = L.tc_paged_attention(*_one_sequence(torch.zeros(rows, 32, dtype=dt), v, torch.ones(2, 32, dtype=dt)))
+            assert bool((out.cpu() == v[0]).all()), out[0, 0, 0]
