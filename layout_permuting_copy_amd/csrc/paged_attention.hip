@@ -208,7 +208,9 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 // PAGE, the rows known to lie on one page: 16 (a half: its address is scalar, its loads go through a
 // buffer resource), 4 (a lane's value rows of a half) or 1.
 //
-// Bound: HBM (a cache row is read once for all heads of its group; FETCH_SIZE counts each byte once).  Measured: one
+// Bound: HBM (a cache row is read once for all heads of its group, up to 16 of them above 128 elements and 32 below;
+// FETCH_SIZE counts each byte once.  Larger groups take their tiles of heads from the cache each: one sequence of 65536 rows of
+// 256, groups of 16 and 20: 95 and 121 us; 131072 rows of 128, 32 and 40: 102 and 143).  Measured: one
 // sequence of 131072 rows, 8 heads of 128 bf16 elements under 64 query heads: 537 MB in 83.4 us (6.4 TB/s, where
 // a plain read of 1 GiB reaches 6.1 through the caches and 7.0 past them); 32 of 16384 8-bit rows: 1.11 GB in 178 us
 // (6.2 TB/s); 64 of mixed lengths up to 4096 in pages that hold a row's heads together: 468 MB in 83 us (5.6).  Short
@@ -853,6 +855,9 @@ void by_dim(const AttentionArgs& a, hipStream_t s) {
 
 int64_t paged_logit_row(int64_t max_len) { return (max_len + dev::kStep - 1) / dev::kStep * dev::kStep; }
 
+// As many runs as make up the workgroups that the card holds at once, to the nearest.  (Where the pairs do not divide those, some
+// workgroups more wait for a second turn: 65536 rows of 256 under 8 heads take 93 us, as many bytes under 6 and 10 heads 138
+// and 142.)
 static int64_t runs_of(int64_t units, int64_t least, int64_t pairs, int64_t resident) {
   const int64_t fit = std::max<int64_t>(1, (resident * dev::kCus + pairs / 2) / pairs);
   return std::min((units + least - 1) / least, fit);
