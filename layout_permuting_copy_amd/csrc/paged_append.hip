@@ -81,9 +81,9 @@ __device__ __forceinline__ void store_row(const u32x4& v, int c, bool active, un
 // move eight values each of the key and of the value (one row a lane: the prompts in 27 us, two 29, four 31).  The rows are
 // on their way while the place of each of the workgroup's tokens is found, once for all its heads: its sequence by a
 // binary search of token_starts (in LDS where they fit), then length, page, offset.
-// Bound: HBM for prompts (16665 tokens of 8 heads of 128: 137 MB in 26.0 us, 5.3 TB/s; new rows are read and cache rows
+// Bound: HBM for prompts (16665 tokens of 8 heads of 128: 137 MB in 25.7 us, 5.3 TB/s; new rows are read and cache rows
 // written past the caches), the latency of starts -> length -> table -> row otherwise (32 single tokens 2.7 us, 6994
-// tokens of 8 heads of 64 to 8 bits 8.5 us).
+// tokens of 8 heads of 64 to 8 bits 8.3 us).
 template <bool BF16, bool E4M3, bool WIDE, int LPR>
 __global__ __launch_bounds__(kAppendThreads) void paged_append_kernel(AppendArgs a, Div32 heads) {
   constexpr int ROWS = kAppendThreads / LPR;

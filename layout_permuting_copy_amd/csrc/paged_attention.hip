@@ -211,10 +211,10 @@ __device__ __forceinline__ Cut cut_of(uint32_t units, uint32_t most, uint32_t le
 // Bound: HBM (a cache row is read once for all heads of its group, up to 16 of them above 128 elements and 32 below;
 // FETCH_SIZE counts each byte once.  Larger groups take their tiles of heads from the cache each: one sequence of 65536 rows of
 // 256, groups of 16 and 20: 95 and 121 us; 131072 rows of 128, 32 and 40: 102 and 143).  Measured: one
-// sequence of 131072 rows, 8 heads of 128 bf16 elements under 64 query heads: 537 MB in 83.4 us (6.4 TB/s, where
-// a plain read of 1 GiB reaches 6.1 through the caches and 7.0 past them); 32 of 16384 8-bit rows: 1.11 GB in 178 us
-// (6.2 TB/s); 64 of mixed lengths up to 4096 in pages that hold a row's heads together: 468 MB in 83 us (5.6).  Short
-// calls are a chain of trips to memory: 131 rows take 6.3 us in a graph, where an empty kernel takes 1.6.  Tried and not
+// sequence of 131072 rows, 8 heads of 128 bf16 elements under 64 query heads: 537 MB in 82.8 us (6.5 TB/s, where
+// a plain read of 1 GiB reaches 6.1 through the caches and 7.0 past them); 32 of 16384 8-bit rows: 1.11 GB in 176 us
+// (6.3 TB/s); 64 of mixed lengths up to 4096 in pages that hold a row's heads together: 468 MB in 83 us (5.6).  Short
+// calls are a chain of trips to memory: 131 rows take 6.5 us in a graph, where an empty kernel takes 1.6.  Tried and not
 // kept: two tiles ahead of the one computed (the short call 7.1 us, the others level), the next sequence's first
 // tile requested before a segment's end (level), fixed splits of 256 to 2048 rows with a join of all (64 sequences:
 // 106 to 143 us).

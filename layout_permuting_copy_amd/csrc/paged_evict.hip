@@ -35,7 +35,7 @@ __device__ __forceinline__ uint32_t sum_below(const uint32_t* x, int wave, int l
 // KEYS: weights a lane holds in registers, with their keys (one read of the weights; THREADS * KEYS rows at most), or
 // 0: every pass reads them again, from the caches.  HISTS: copies of the histogram, one for every HISTS-th wave, so that
 // fewer lanes add to one bin.  Bound: trips to memory, barriers, LDS atomics and, with many rows, the vector
-// instructions of one workgroup's walks (8 heads of 2049 rows 6.6 us, 128 of up to 16384 rows 15.5 us; with the keys made
+// instructions of one workgroup's walks (8 heads of 2049 rows 6.5 us, 128 of up to 16384 rows 15.4 us; with the keys made
 // again by every walk 20 us, with the weights read again by every pass 33 us).
 template <int THREADS, int KEYS, int HISTS>
 __global__ __launch_bounds__(THREADS) void paged_select_kernel(EvictArgs a, Div32 heads) {
