@@ -453,6 +453,70 @@ int tc_paged_evict(const tc_paged_cache* src, const int32_t* block_table, const 
                    int64_t budget, int64_t recent, int32_t* lens_out, int32_t* kept, const tc_layout* kept_layout,
                    float* weights_out, const tc_layout* weights_out_layout, void* stream);
 
+/*
+ * Grows and shrinks sequences: sequence b goes from n = max(0, seq_lens[b]) rows to n + change[b] (at least 0, at most 2^31 - 1),
+ * and its row of the block table (batch, columns), updated in place, from the pages that n rows take to those that the new
+ * ones do (no more than it has columns).  free_pages[0 .. free_count[0] - 1] is a stack of free pages (free_count is taken as at
+ * least 0 and at most free_capacity): the pages that sequences give up, in the order of b and of their columns, are put onto it
+ * as far as it has room (entries below 0 are no pages); then those needed are taken off its top, in the same order.  An entry
+ * for which none is left becomes -1.  Entries past a sequence's new rows keep what they held, pages given up among them.  A
+ * page that two shrinking sequences name is put onto the stack twice: shared pages are the caller's to count.
+ *   lens_out, count_out   the new lengths (batch, contiguous) and count; may be seq_lens and free_count themselves
+ *   missing               may be NULL: how many pages were needed that the stack did not have
+ *   token_starts          (batch + 1), may be NULL: where each sequence's new rows begin, counted over all sequences in order
+ *                         (sums stop at 2^31 - 1)
+ *   slots, positions      (tokens), may be NULL, both need token_starts: for each new row its place page * page_size + row of the
+ *                         page, or -1 on no page, and its row in the sequence; both -1 from token_starts[batch] on
+ * Everything lies on the device.  Errors: TC_E_NULL, TC_E_RANK, TC_E_EXTENT, TC_E_ALIGN, TC_E_NONINJECTIVE, TC_E_ALIAS,
+ * TC_E_ARG, TC_E_RANGE (more than 2^31 - 1 table entries), TC_E_HIP.
+ */
+int tc_paged_resize(int32_t* block_table, const tc_layout* table_layout, const int32_t* seq_lens, const int32_t* change,
+                    int64_t page_size, int32_t* free_pages, int64_t free_capacity, const int32_t* free_count, int32_t* lens_out,
+                    int32_t* count_out, int32_t* missing, int32_t* token_starts, int64_t* slots, int32_t* positions, int64_t tokens,
+                    void* stream);
+
+/*
+ * Attention of each sequence's last tokens over its cache.  q, out: (tokens, q_heads, head_dim) of `dtype` (TC_F16 or TC_BF16: the
+ * cache's type, or either over a TC_E4M3 cache), rows on 16-byte boundaries; token_starts (batch + 1, contiguous, ascending) as
+ * in tc_paged_append: token i of the t = starts[b + 1] - starts[b] of sequence b is its row n - t + i, n = seq_lens[b] (at
+ * most max_len).  With masks (tokens, contiguous), for drafted trees, it sees the rows below n - t and rows n - t + j for the set bits
+ * j of masks[starts[b] + i] (its own row by its own bit only; j < 64, t may be larger); without (NULL), rows 0 .. n - t + i.
+ * Over the rows it sees, x, lse and out are those of tc_paged_attention, sums and maxima in fp32; none, or none with x above
+ * -infinity: out = 0, lse = -infinity.  The weights are rounded to the type of the second product (the cache's; bf16 for TC_E4M3),
+ * relative to a reference that lags the maximum by 2^8 at most, as one value or, where few query rows share a sequence's cache,
+ * as the sum of two.  Rows that are not seen, past n or on no page are never used, whatever they hold; an infinite or NaN value
+ * in a row that is seen makes its element of out infinite or NaN.  Equal calls give equal bits; how rows are dealt out, and with it
+ * the last bits of sums, depends on the whole batch and max_len.  Tokens from starts[batch] on are padding: their rows of out and lse
+ * are left as they are.  lse (tokens, q_heads), fp32, may be NULL.
+ * workspace: tc_paged_tree_attention_workspace(...) bytes of device memory (a call may use fewer), 16-byte aligned, used until
+ * the call's kernels end and by no other call meanwhile; may be NULL where that is 0.
+ * Errors: as tc_paged_attention; TC_E_RANGE also for tokens * q_heads beyond 2^30.
+ */
+int tc_paged_tree_attention(const tc_paged_cache* cache, const void* q, const tc_layout* q_layout, void* out,
+                            const tc_layout* out_layout, int dtype, const int32_t* block_table, const tc_layout* table_layout,
+                            const int32_t* seq_lens, const int32_t* token_starts, const int64_t* masks, int64_t max_len, float scale,
+                            float* lse, const tc_layout* lse_layout, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that suffice for tc_paged_tree_attention at these sizes and at any smaller batch, tokens and max_len (0: none
+ * is needed), or a negative status.  Host only. */
+int64_t tc_paged_tree_attention_workspace(int64_t batch, int64_t tokens, int64_t q_heads, int64_t heads, int64_t head_dim,
+                                          int64_t max_len);
+
+/*
+ * Attention of whole prompts, packed: q, out (tokens, q_heads, head_dim) and k, v (keys, heads, head_dim) of `dtype` TC_F16 or
+ * TC_BF16, any token and head strides (slices of a fused projection's rows), innermost stride 1, rows on 16-byte boundaries,
+ * keys and values less than 2^24 bytes apart from token to token.  q_heads = group * heads, query head h reads head h / group.
+ * Tokens token_starts[b] .. token_starts[b + 1] - 1 (batch + 1 entries, contiguous, ascending, on the device) are sequence b, keys
+ * key_starts[b] .. likewise (NULL: token_starts, keys == tokens).  With causal = 1 token i of n sees keys 0 .. m - n + i of m (its
+ * sequence's last token all of them; none where that is below 0), with 0 all m.  x, lse, out, their precision (weights as one value) and
+ * what becomes of rows that are not seen, of padding and of infinities are those of tc_paged_tree_attention.
+ * Errors: as above.
+ */
+int tc_prompt_attention(const void* q, const tc_layout* q_layout, const void* k, const tc_layout* k_layout, const void* v,
+                        const tc_layout* v_layout, void* out, const tc_layout* out_layout, int dtype, int64_t batch,
+                        const int32_t* token_starts, const int32_t* key_starts, int causal, float scale, float* lse,
+                        const tc_layout* lse_layout, void* stream);
+
 /* Library version, major * 10000 + minor * 100 + patch. */
 int tc_version(void);
 

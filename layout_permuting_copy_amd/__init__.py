@@ -4,7 +4,8 @@ Thin ctypes marshalling over the C ABI declared in ``include/tile_copy.h``; ever
 the copy (planning, kernels) runs in the native library.  Names match the C entry points:
 ``tile_copy``, ``tile_copy_ex``, ``tc_plan``, ``tc_last_error``, ``tc_set_flags``,
 ``tc_get_flags``, ``tc_layout_slice``, ``tc_version``, ``tc_paged_append``, ``tc_paged_attention``,
-``tc_paged_evict`` (these three take torch tensors and a ``PagedCache``).
+``tc_paged_evict``, ``tc_paged_resize``, ``tc_paged_tree_attention`` and ``tc_prompt_attention`` (these take torch tensors
+and, over a cache, a ``PagedCache``).
 
 Layouts are ``(shape, stride, offset)`` tuples in elements (TileLayout S[shape : stride]),
 or ``TcLayout`` structs.  Source and destination are device pointers (ints) or torch
@@ -167,6 +168,14 @@ def load_library(path: str = LIB_PATH):
     lib.tc_paged_attention.restype = ctypes.c_int
     lib.tc_paged_evict.argtypes = [vp, vp, lp, vp, i64, vp, lp, vp, vp, lp, i64, i64, vp, vp, lp, vp, lp, vp]
     lib.tc_paged_evict.restype = ctypes.c_int
+    lib.tc_paged_resize.argtypes = [vp, lp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.tc_paged_resize.restype = ctypes.c_int
+    lib.tc_prompt_attention.argtypes = [vp, lp, vp, lp, vp, lp, vp, lp, i32, i64, vp, vp, i32, ctypes.c_float, vp, lp, vp]
+    lib.tc_prompt_attention.restype = ctypes.c_int
+    lib.tc_paged_tree_attention_workspace.argtypes = [i64] * 6
+    lib.tc_paged_tree_attention_workspace.restype = ctypes.c_int64
+    lib.tc_paged_tree_attention.argtypes = [vp, vp, lp, vp, lp, i32, vp, lp, vp, vp, vp, i64, ctypes.c_float, vp, lp, vp, i64, vp]
+    lib.tc_paged_tree_attention.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -410,20 +419,20 @@ class PagedCache:
 
 
 _torch = _here = _raw_stream = None
-_T_I32 = _T_F32 = None
+_T_I32 = _T_I64 = _T_F32 = None
 _PAGED_DTYPES = {}
 
 
 def _import_torch():
     """torch and the types the paged entry points name, looked up once."""
-    global _torch, _T_I32, _T_F32, _here, _raw_stream
+    global _torch, _T_I32, _T_I64, _T_F32, _here, _raw_stream
     if _torch is None:
         import torch
         # the current device and stream without the public calls' wrappers (0.1 us each; current_stream() takes 2.5)
         _here = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                        or (lambda index: torch.cuda.current_stream(index).cuda_stream))
-        _T_I32, _T_F32 = torch.int32, torch.float32
+        _T_I32, _T_I64, _T_F32 = torch.int32, torch.int64, torch.float32
         _PAGED_DTYPES.update({torch.float16: TC_F16, torch.bfloat16: TC_BF16, torch.float8_e4m3fn: TC_E4M3})
         _torch = torch
     return _torch
@@ -449,9 +458,10 @@ def _device_of(cache, *tensors):
     return dev
 
 
-def _vector(name: str, x, n: int) -> int:
-    if x.dtype != _T_I32 or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
-        raise ValueError(f"{name} must be int32, contiguous, with {n} elements, got {x.dtype} {tuple(x.shape)}")
+def _vector(name: str, x, n: int, dtype=None) -> int:
+    if x.dtype != (dtype or _T_I32) or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} must be {'int64' if dtype else 'int32'}, contiguous, with {n} elements, got {x.dtype} "
+                         f"{tuple(x.shape)}")
     return x.data_ptr()
 
 
@@ -653,3 +663,172 @@ def tc_paged_evict(src: PagedCache, block_table, seq_lens, weights, dst: PagedCa
     if rc != TC_OK:
         _check(rc)
     return lens_out, kept
+
+
+def tc_paged_resize(block_table, seq_lens, change, free_pages, free_count, page_size: int, lens_out=None, count_out=None,
+                    token_starts=None, slots=None, positions=None, missing=None, stream=None):
+    """Grows and shrinks the sequences of a block table by ``change`` (batch) int32 rows each (negative: rows are dropped from
+    the end, at most all), taking pages off a stack of free ones and putting those back that are no longer needed.
+
+    ``free_pages`` (capacity) int32 holds the free pages, ``free_count`` (1) int32 how many; the last is taken first.  Pages that
+    come back are put onto it before any is taken, sequence by sequence and in the table's order, as pages are taken.
+    ``block_table`` (batch, columns) int32 is updated in place: entries past a sequence's rows keep what they held, an entry
+    for which no page is left becomes -1 (``missing`` (1) int32 receives their number).  ``lens_out`` (default: ``seq_lens``
+    itself) and ``count_out`` (default: ``free_count`` itself) receive the new lengths and count.
+
+    For the rows that sequences grow by, ``token_starts`` (batch + 1) int32 receives where each sequence's begin when they are
+    listed one after another, as `tc_paged_append` takes them; ``slots`` (tokens) int64 their places in the pool (page *
+    page_size + row of the page, -1 on no page) and ``positions`` (tokens) int32 their rows in the sequence, both -1 past the
+    last.  These two need ``token_starts``.  Returns ``lens_out``."""
+    lib = _lib or load_library()
+    _import_torch()
+    dev = _device_of(block_table, seq_lens, change, free_pages, free_count, lens_out, count_out, token_starts, slots, positions,
+                     missing)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be (batch, columns)")
+    _want("block_table", block_table, _T_I32)
+    batch = block_table.shape[0]
+    if lens_out is None:
+        lens_out = seq_lens
+    if count_out is None:
+        count_out = free_count
+    tokens, sp, pp, tp, mp = 0, None, None, None, None
+    if slots is not None:
+        tokens = slots.numel()
+        sp = _vector("slots", slots, tokens, _T_I64)
+    if positions is not None:
+        if slots is not None and positions.numel() != tokens:
+            raise ValueError(f"slots has {tokens} elements, positions {positions.numel()}")
+        tokens = positions.numel()
+        pp = _vector("positions", positions, tokens)
+    if token_starts is not None:
+        tp = _vector("token_starts", token_starts, batch + 1)
+    if missing is not None:
+        mp = _vector("missing", missing, 1)
+    capacity = free_pages.numel()
+    tl = _lay(block_table)
+    back = _enter(dev)
+    try:
+        rc = lib.tc_paged_resize(block_table.data_ptr(), tl[0], _vector("seq_lens", seq_lens, batch), _vector("change", change, batch),
+                                 page_size, _vector("free_pages", free_pages, capacity), capacity,
+                                 _vector("free_count", free_count, 1), _vector("lens_out", lens_out, batch),
+                                 _vector("count_out", count_out, 1), mp, tp, sp, pp, tokens,
+                                 _raw_stream(dev.index) if stream is None else _stream(stream))
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != TC_OK:
+        _check(rc)
+    return lens_out
+
+
+def tc_prompt_attention(q, k, v, token_starts, key_starts=None, causal: bool = True, scale: Optional[float] = None, out=None,
+                        lse=None, stream=None):
+    """Attention of packed sequences, ``q`` (tokens, q_heads, head_dim) over ``k``, ``v`` (keys, heads, head_dim), float16 or
+    bfloat16 with any outer strides (slices of a fused projection's rows); returns ``out``, of q's shape.
+
+    ``token_starts`` (batch + 1) int32: tokens starts[b] .. starts[b + 1] - 1 are sequence b; ``key_starts`` (default:
+    ``token_starts`` itself) the same of its keys.  ``causal``: a sequence's last token sees all of its keys, the one before all
+    but the last, and so on (a token that sees none has an out of 0 and an lse of -infinity).  ``scale`` defaults to
+    head_dim ** -0.5.  ``lse`` (tokens, q_heads) float32 receives the log of the sums.  Rows of ``out`` and ``lse`` past the
+    last sequence are left as they are (not set, in an ``out`` that the call makes).
+
+    No gradient is formed: ``out`` is not part of ``q``'s graph, whether or not ``q`` requires a gradient."""
+    lib = _lib or load_library()
+    _import_torch()
+    dev = _device_of(q, k, v, token_starts, key_starts, out, lse)
+    if q.dtype != k.dtype or q.dtype != v.dtype:
+        raise ValueError(f"q is {q.dtype}, k {k.dtype}, v {v.dtype}")
+    if q.dim() != 3 or token_starts.dim() != 1 or token_starts.numel() < 1:
+        raise ValueError("q must be (tokens, q_heads, head_dim), token_starts (batch + 1)")
+    batch = token_starts.numel() - 1
+    starts = _vector("token_starts", token_starts, batch + 1)
+    key_at = None if key_starts is None else _vector("key_starts", key_starts, batch + 1)
+    ll, lp = _NONE, None
+    if lse is not None:
+        _want("lse", lse, _T_F32)
+        ll, lp = _lay(lse), lse.data_ptr()
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+    code = _paged_dtype(q)
+    ql, kl, vl = _lay(q), _lay(k), _lay(v)
+    back = _enter(dev)
+    try:
+        handle = _raw_stream(dev.index) if stream is None else _stream(stream)
+        if out is None:
+            out = _empty_on(handle, dev, q.shape, q.dtype)
+        elif out.dtype != q.dtype:
+            raise ValueError(f"out is {out.dtype}, q {q.dtype}")
+        ol = _lay(out)
+        rc = lib.tc_prompt_attention(q.data_ptr(), ql[0], k.data_ptr(), kl[0], v.data_ptr(), vl[0], out.data_ptr(), ol[0], code, batch,
+                                     starts, key_at, 1 if causal else 0, scale, lp, ll[0], handle)
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != TC_OK:
+        _check(rc)
+    return out
+
+
+_tree_workspace_cache = {}
+
+
+def tc_paged_tree_attention(q, cache: PagedCache, block_table, seq_lens, token_starts, masks=None, scale: Optional[float] = None,
+                            max_len: Optional[int] = None, out=None, lse=None, stream=None):
+    """Attention of each sequence's last tokens, ``q`` (tokens, q_heads, head_dim), over its cached rows, theirs among them;
+    returns ``out``, of q's shape.
+
+    ``token_starts`` (batch + 1) int32: tokens starts[b] .. starts[b + 1] - 1 are the last rows of sequence b, in order, as
+    `tc_paged_append` takes them.  ``masks`` (tokens) int64, for trees of drafted tokens: a token sees all rows before its
+    sequence's tokens and, of these, token j where bit j is set (itself only by its own bit; tokens from the 65th on are seen by
+    none).  Without masks a token sees the rows up to its own: a chunk of a prompt.  ``scale``, ``lse``, ``max_len`` as in
+    `tc_paged_attention`, ``lse`` of shape (tokens, q_heads); rows of ``out`` and ``lse`` past the last sequence are left as
+    they are (not set, in an ``out`` that the call makes).
+
+    No gradient is formed: ``out`` is not part of ``q``'s graph, whether or not ``q`` requires a gradient."""
+    lib = _lib or load_library()
+    dev = _device_of(cache, q, block_table, seq_lens, token_starts, masks, out, lse)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be (tokens, q_heads, head_dim), block_table (batch, columns)")
+    _want("block_table", block_table, _T_I32)
+    tokens, q_heads, dim = q.shape
+    batch = block_table.shape[0]
+    lens, starts = _vector("seq_lens", seq_lens, batch), _vector("token_starts", token_starts, batch + 1)
+    words = None if masks is None else _vector("masks", masks, tokens, _T_I64)
+    if max_len is None:
+        max_len = block_table.shape[1] * cache.page_size
+    if scale is None:
+        scale = dim ** -0.5
+    ll, lp = _NONE, None
+    if lse is not None:
+        _want("lse", lse, _T_F32)
+        ll, lp = _lay(lse), lse.data_ptr()
+    code = _paged_dtype(q)
+    ql, tl = _lay(q), _lay(block_table)
+    back = _enter(dev)
+    try:
+        handle = _raw_stream(dev.index) if stream is None else _stream(stream)
+        if out is None:
+            out = _empty_on(handle, dev, q.shape, q.dtype)
+        elif out.dtype != q.dtype:
+            raise ValueError(f"out is {out.dtype}, q {q.dtype}")
+        ol = _lay(out)
+        key = (batch, tokens, q_heads, cache.heads, dim, max_len)
+        need = _tree_workspace_cache.get(key)
+        if need is None:
+            need = lib.tc_paged_tree_attention_workspace(*key)
+            if need < 0:
+                _check(need)
+            if len(_tree_workspace_cache) >= 4096:
+                _tree_workspace_cache.clear()
+            _tree_workspace_cache[key] = need
+        work = _empty_on(handle, dev, need, _torch.uint8) if need else None
+        rc = lib.tc_paged_tree_attention(cache._ref, q.data_ptr(), ql[0], out.data_ptr(), ol[0], code, block_table.data_ptr(), tl[0],
+                                         lens, starts, words, max_len, scale, lp, ll[0],
+                                         None if work is None else work.data_ptr(), need, handle)
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != TC_OK:
+        _check(rc)
+    return out

@@ -27,7 +27,9 @@ RESOURCES = os.path.join(BUILD, "kernel_resources.json")
 REMARK = ["-Rpass-analysis=kernel-resource-usage"]
 SOURCES = ["layout.cpp", "bank.cpp", "plan.cpp", "permute.cpp", "abi.cpp", "kernels.hip", "transpose_eb1.hip", "transpose_eb2.hip",
            "transpose_eb4.hip", "transpose_eb8.hip", "transpose_eb16.hip", "paged_abi.cpp", "paged_append.hip",
-           "paged_attention.hip", "paged_evict.hip"]
+           "paged_attention.hip", "paged_evict.hip", "paged_resize.hip", "rows_abi.cpp", "rows_shape.cpp", "prompt_attention.hip",
+           "tree_attention.hip", "tree_attention_f16.hip", "tree_attention_bf16.hip", "tree_attention_e4m3_f16.hip",
+           "tree_attention_e4m3_bf16.hip"]
 
 
 def _run(cmd):

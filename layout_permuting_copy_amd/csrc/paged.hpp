@@ -83,6 +83,33 @@ struct AttentionArgs {
   float scale_log2e;
 };
 
+// Attention of several query rows a sequence, over packed keys and values (k, v; key_starts) or a paged cache (pool, table,
+// lens).  Byte strides of tokens and heads.
+struct RowsArgs {
+  PagedPool pool;
+  PagedTable table;
+  const int32_t* lens;
+  const unsigned char* k;
+  const unsigned char* v;
+  int64_t kt, kh, vt, vh;
+  const int32_t* key_starts;
+  const unsigned char* q;
+  unsigned char* out;
+  int64_t qt, qh, ot, oh;
+  float* lse;  // or NULL
+  int64_t lt, lh;
+  const int32_t* starts;
+  const int64_t* masks;  // or NULL: a token sees the rows up to its own, where causal
+  float* part_o;         // [workgroups][tile rows][head_dim]: a part's sum of p v, relative to its maximum
+  float* part_ml;        // [workgroups][tile rows][2]: its maximum (of q k) and sum
+  int32_t batch, tokens, key_rows, heads, group, head_dim, max_len, causal;
+  int32_t slots, least;  // workgroups that the parts of tiles should fill (0: tiles are whole), units a part has at least
+  int64_t tiles, workgroups;  // at most: tiles of all sequences, workgroups of the call
+  Div32 group_div, heads_div;
+  float scale, scale_log2e;  // of |scale|: its sign is q's (q_xor), a scale of 0 is a q of 0 (q_and)
+  uint32_t q_and, q_xor;
+};
+
 struct EvictArgs {
   PagedPool src, dst;
   PagedTable table, dst_table;
@@ -98,6 +125,23 @@ struct EvictArgs {
   int32_t max_len, budget, recent;
 };
 
+struct ResizeArgs {
+  PagedTable table;
+  int32_t* table_out;  // its entries
+  const int32_t* lens;
+  const int32_t* change;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* lens_out;
+  int32_t* count_out;
+  int32_t* missing;    // or NULL
+  int32_t* starts;     // or NULL, as slots and positions
+  int64_t* slots;
+  int32_t* positions;
+  int32_t capacity, tokens;
+  Div32 page;
+};
+
 // How an attention call is cut over the cache's length: units of `unit_rows` rows (at most `units` in all), `runs` runs
 // of at least least_units of them, query heads in tiles of tile_heads, at most `workgroups` workgroups; whether a
 // sequence's rows can fall to more than one run.  `most`: as a call of a smaller batch may be cut where this one is not, so
@@ -110,6 +154,15 @@ PagedCut paged_cut(int64_t batch, int64_t heads, int64_t group, int64_t head_dim
 // Columns a row of the logits workspace holds: max_len rounded up to whole tiles.
 int64_t paged_logit_row(int64_t max_len);
 
+// How a call of attention of several rows is dealt out: query rows in tiles of tile_rows, key rows in units of unit_rows, the
+// card filled by parts of tiles (slots, least as in RowsArgs) where tiles are few.
+struct RowsShape {
+  int64_t tile_rows, unit_rows, tiles, slots, least, workgroups;
+};
+RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
+// Bytes that suffice for the parts of tiles at these sizes and at any smaller batch, tokens and max_len.
+int64_t rows_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
+
 // A launch counts its lanes in 32 bits.
 constexpr bool launchable(int64_t workgroups, int64_t threads) { return workgroups * threads < int64_t(1) << 32; }
 
@@ -118,5 +171,8 @@ constexpr bool launchable(int64_t workgroups, int64_t threads) { return workgrou
 int launch_paged_append(const AppendArgs& a, int dtype, int cache_dtype, bool wide, void* stream);
 int launch_paged_attention(const AttentionArgs& a, int dtype, int cache_dtype, void* stream);
 int launch_paged_evict(const EvictArgs& a, int cache_dtype, void* stream);
+int launch_prompt_attention(const RowsArgs& a, const RowsShape& shape, int dtype, void* stream);
+int launch_tree_attention(const RowsArgs& a, const RowsShape& shape, int dtype, int cache_dtype, void* stream);
+int launch_paged_resize(const ResizeArgs& a, void* stream);
 
 }  // namespace tc

@@ -7,19 +7,12 @@
 namespace tc {
 namespace dev {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = 4;
 constexpr int kTile = 32;                       // cache rows a wave takes at a time
 constexpr int kStep = kTile * kAttnWaves;       // and a workgroup
 constexpr int kJoinThreads = 256;
 constexpr int kCus = 256;
-constexpr float kInf = __builtin_inff();
 
 // N bytes of a buffer resource at a lane's offset, `more` bytes on: zeros past its range, which takes the place of a condition
 // on the load (every wait then is for a fixed number of younger loads).  STREAM: read past the caches.
@@ -51,62 +44,6 @@ __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Two fp32 values to two of the 16-bit type, nearest even.
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (BF16) {
-    bf16x2 v;
-    v[0] = __bf16(x);
-    v[1] = __bf16(y);
-    return __builtin_bit_cast(uint32_t, v);
-  } else {
-    f16x2 v;
-    v[0] = _Float16(x);
-    v[1] = _Float16(y);
-    return __builtin_bit_cast(uint32_t, v);
-  }
-}
-template <bool BF16>
-__device__ __forceinline__ float low_half(uint32_t v) {
-  if constexpr (BF16) return __builtin_bit_cast(float, v << 16);
-  return float(__builtin_bit_cast(f16x2, v)[0]);
-}
-template <bool BF16>
-__device__ __forceinline__ float high_half(uint32_t v) {
-  if constexpr (BF16) return __builtin_bit_cast(float, v & 0xffff0000u);
-  return float(__builtin_bit_cast(f16x2, v)[1]);
-}
-
-// Two e4m3 codes (the low or high half of w) to two values of the 16-bit type: exact in both.
-template <bool BF16, bool HIGH>
-__device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
-  if constexpr (BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
-}
-
-// The maximum as the exponents' reference, kept finite: exp2(x - reference) is then 0 for x = -infinity and
-// infinite for x = +infinity, so a row of nothing sums to 0 and an infinite logit to infinity (its lse; out,
-// infinity over infinity, is NaN).
-__device__ __forceinline__ float finite(float top) {
-  return __builtin_amdgcn_fmed3f(top, -3.4028234664e38f, 3.4028234664e38f);
-}
-
-// x of this lane's pair and of the lane 16 (D = 16) or 32 away, in either order: a register swapped with a copy of
-// itself by rows or halves.  The copy has to be a register of its own.
-template <int D>
-__device__ __forceinline__ void partners(float x, float* p, float* q) {
-  uint32_t a = __builtin_bit_cast(uint32_t, x), b = a;
-  asm("" : "+v"(b));
-  if constexpr (D == 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0], b = r[1];
-  } else {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0], b = r[1];
-  }
-  *p = __builtin_bit_cast(float, a);
-  *q = __builtin_bit_cast(float, b);
-}
 // The maximum or sum over the four lanes that differ in bits 4 and 5 (the groups g).
 __device__ __forceinline__ float max_of_groups(float x) {
   float p, q;

@@ -1,0 +1,26 @@
+// Attention of each sequence's last tokens over its paged cache: the instances of one pair of types.
+#pragma once
+
+#include "rows_launch.hpp"
+
+namespace tc {
+namespace dev {
+
+template <bool BF16, int SRC, int DP, int PARTS>
+void tree_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
+  if constexpr (DP <= 128)
+    if (shape.tile_rows == 32) return attend_rows<BF16, SRC, DP, 1, 1, PARTS>(a, s);
+  if (shape.tile_rows <= 64) return attend_rows<BF16, SRC, DP, 1, 2, PARTS>(a, s);
+  return attend_rows<BF16, SRC, DP, 1, 4, 1>(a, s);
+}
+
+template <bool BF16, int SRC>
+void tree_by_dim(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
+  constexpr int PARTS = BF16 || SRC == 2 ? 2 : 1;
+  if (a.head_dim <= 64) return tree_by_tile<BF16, SRC, 64, PARTS>(a, shape, s);
+  if (a.head_dim <= 128) return tree_by_tile<BF16, SRC, 128, PARTS>(a, shape, s);
+  return tree_by_tile<BF16, SRC, 256, PARTS>(a, shape, s);
+}
+
+}  // namespace dev
+}  // namespace tc
