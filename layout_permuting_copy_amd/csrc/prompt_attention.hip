@@ -16,7 +16,9 @@ void prompt_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
 template <bool BF16>
 void prompt_by_dim(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
   if (a.head_dim <= 64) return prompt_by_tile<BF16, 64>(a, shape, s);
+  if (a.head_dim <= 96) return prompt_by_tile<BF16, 96>(a, shape, s);
   if (a.head_dim <= 128) return prompt_by_tile<BF16, 128>(a, shape, s);
+  if (a.head_dim <= 192) return prompt_by_tile<BF16, 192>(a, shape, s);
   return prompt_by_tile<BF16, 256>(a, shape, s);
 }
 

@@ -245,9 +245,10 @@ struct Rows {
   static constexpr bool ACC = RESIDENT == 1;
 
   // Which 16-byte chunk of a row lies at place c of its row in LDS, and the other way round (an exchange): the rows that one
-  // access reads at the same chunk, eight of keys (16 bytes a lane) and four or, of 8-bit values, eight (transposed, half a
+  // access reads at the same chunk, sixteen of keys (16 bytes a lane) and four or, of 8-bit values, eight (transposed, half a
   // chunk a lane), lie in different banks.
-  static __device__ __forceinline__ int key_chunk(int row, int c) { return c ^ (PB == 64 ? row >> 2 & 3 : row & 7); }
+  static constexpr int KX = CPR < 16 ? CPR : 16;  // chunks that a key row's exchange covers: 16 rows at 16 places
+  static __device__ __forceinline__ int key_chunk(int row, int c) { return c ^ (row / (PB < 256 ? 256 / PB : 1) & (KX - 1)); }
   static __device__ __forceinline__ int value_chunk(int row, int c) {
     if constexpr (E4M3) return c ^ (PB == 64 ? (row >> 3 & 1) << 1 : (row & 3) | (row >> 3 & 1) << 2);
     return c ^ (PB == 128 ? row >> 1 & 1 : row & 3) << 2;
@@ -443,10 +444,12 @@ void rows_attention_kernel(RowsArgs a) {
   // What a lane reads of LDS, from a tile's first row of 32 (keys) or 16 (values) on.  Keys: row r, the 16 bytes of step k (of
   // two steps of 8-bit elements).  Values: see read_transposed; the rows of a lane's element j are 4 hl + j (j < 4) and
   // 4 hl + 8 + j - 4, which is how S^T's rows lie in registers
-  int kbase[4], vbase[4];
+  constexpr int KB = C::KX / 2;
+  int kbase[KB], vbase[4];
+#pragma unroll
+  for (int j = 0; j < KB; ++j) kbase[j] = r * PB + C::key_chunk(r, 2 * j + hl) * 16;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    kbase[j] = r * PB + C::key_chunk(r, (2 * j + hl) % C::CPR) * 16;
     const int i = lane & 15, g = lane >> 4 & 1;
     if constexpr (E4M3) {
       const int row = 4 * hl + (i >> 1 & 3) + (i >> 3) * 8;
@@ -456,14 +459,9 @@ void rows_attention_kernel(RowsArgs a) {
       vbase[j] = row * PB + C::value_chunk(row, (4 * j + 2 * g + (i >> 1 & 1)) % C::CPR) * 16 + (i & 1) * 8;
     }
   }
-  // (the exchanges stay among the chunks that the four bases cover)
-  const auto key_operand = [&](const unsigned char* at, int k) {
-    if constexpr (E4M3) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(at + kbase[(k >> 1) & 3] + (k >> 3) * 128 + (k & 1) * 8);
-      return u32x4{from_e4m3<BF16, false>(w[0]), from_e4m3<BF16, true>(w[0]), from_e4m3<BF16, false>(w[1]), from_e4m3<BF16, true>(w[1])};
-    } else {
-      return *reinterpret_cast<const u32x4*>(at + kbase[k & 3] + (k >> 2) * 128);
-    }
+  // (the exchanges stay among the chunks that the bases cover)
+  const auto key_words = [&](const unsigned char* at, int j) {
+    return *reinterpret_cast<const u32x4*>(at + kbase[j % KB] + j / KB * 256);
   };
   const auto value_operand = [&](const unsigned char* at, int f) {
     if constexpr (E4M3) {
@@ -587,10 +585,18 @@ void rows_attention_kernel(RowsArgs a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[t][n][i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const u32x4 y = key_operand(base, k);
+        for (int j = 0; j < (E4M3 ? KS / 2 : KS); ++j) {
+          const u32x4 w = key_words(base, j);
 #pragma unroll
-          for (int t = 0; t < QT; ++t) s[t][n] = mfma32<BF16>(y, q[t][k], s[t][n]);
+          for (int half = 0; half < (E4M3 ? 2 : 1); ++half) {
+            u32x4 y = w;
+            if constexpr (E4M3) {
+              const uint32_t lo = w[2 * half], hi = w[2 * half + 1];
+              y = u32x4{from_e4m3<BF16, false>(lo), from_e4m3<BF16, true>(lo), from_e4m3<BF16, false>(hi), from_e4m3<BF16, true>(hi)};
+            }
+#pragma unroll
+            for (int t = 0; t < QT; ++t) s[t][n] = mfma32<BF16>(y, q[t][E4M3 ? 2 * j + half : j], s[t][n]);
+          }
         }
       }
 
