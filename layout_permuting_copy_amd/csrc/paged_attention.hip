@@ -304,12 +304,6 @@ struct Attend {
   }
 };
 
-// A lane number as it is: what derives from it at one end of a segment is not kept in registers until the next.
-__device__ __forceinline__ int fresh(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-
 // The kernel's arguments, read again from where they lie: what only the end of a segment needs is
 // not held in scalar registers through the loop (there are about a hundred, and what spills costs vector registers).
 __device__ __forceinline__ const AttentionArgs& arguments_again() {

@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
   return x;
 }
 
+// A number as it is, but not as known: what derives from it is computed anew, not kept in registers from before.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // The greatest of N neighbouring lanes' x (N = 2 .. 32, a power of two), in each of them: swaps within four lanes, then
 // mirrors of 8 and 16 (whose halves hold equal values by then).
 template <int N>

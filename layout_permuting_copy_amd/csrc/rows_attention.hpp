@@ -221,7 +221,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 template <bool BF16, int SRC, int DP, int QT, int WQ, int PARTS>
 struct Rows {
   static constexpr bool PAGED = SRC != 0, E4M3 = SRC == 2, VBF = BF16 || E4M3;
-  static constexpr int NG = 4 / WQ;
+  static constexpr int WAVES = WQ > 4 ? WQ : 4, THREADS = 64 * WAVES;
+  static constexpr int NG = WAVES / WQ;
   static constexpr int KT = NG == 4 ? 128 : 64;   // key rows a turn
   static constexpr int NSUB = KT / 32 / NG;       // of them 32 at a time a wave
   static constexpr int NJ = DP > 128 || QT > 1 || E4M3 ? 1 : NSUB;  // of these at once: what the registers hold
@@ -232,17 +233,17 @@ struct Rows {
   static constexpr int KS = DP / 16, NF = DP / 32;
   static constexpr int CPR = PB / 16;             // lanes that load a row, 16 bytes each
   static constexpr int RPW = 64 / CPR;            // rows a wave loads at once
-  static constexpr int RPP = 4 * RPW;             // and a workgroup
+  static constexpr int RPP = WAVES * RPW;             // and a workgroup
   static constexpr int PASSES = KT / RPP;
   static constexpr int RAISE = VBF ? 0 : 7;
   static constexpr int TILE_BYTES = KT * PB;
   static constexpr int OP = DP + 4;               // floats a row of the waves' meeting
-  static constexpr int MERGE_BYTES = NG == 1 ? 0 : 4 * 32 * OP * 4;
+  static constexpr int MERGE_BYTES = NG == 1 ? 0 : WAVES * 32 * OP * 4;
   static_assert(NG == 1 || QT == 1, "waves that share rows have one tile each");
   static constexpr int LDS_BYTES = 4 * TILE_BYTES > MERGE_BYTES ? 4 * TILE_BYTES : MERGE_BYTES;
-  // Workgroups that a compute unit holds, by their registers and LDS; a wave of a single one has accumulation registers.
-  static constexpr int RESIDENT = QT == 1 && DP <= 128 && LDS_BYTES <= 80 * 1024 ? 2 : 1;
-  static constexpr bool ACC = RESIDENT == 1;
+  // Workgroups that a compute unit holds, by their registers and LDS; a wave that has a SIMD to itself has accumulation registers.
+  static constexpr int RESIDENT = WAVES == 4 && QT == 1 && DP <= 128 && LDS_BYTES <= 80 * 1024 ? 2 : 1;
+  static constexpr bool ACC = RESIDENT * WAVES == 4;
 
   // Which 16-byte chunk of a row lies at place c of its row in LDS, and the other way round (an exchange): the rows that one
   // access reads at the same chunk, sixteen of keys (16 bytes a lane) and four or, of 8-bit values, eight (transposed, half a
@@ -261,7 +262,7 @@ struct Rows {
 };
 
 template <bool BF16, int SRC, int DP, int QT, int WQ, int PARTS>
-__global__ __launch_bounds__(kRowsThreads, (Rows<BF16, SRC, DP, QT, WQ, PARTS>::RESIDENT))
+__global__ __launch_bounds__((Rows<BF16, SRC, DP, QT, WQ, PARTS>::THREADS), (Rows<BF16, SRC, DP, QT, WQ, PARTS>::RESIDENT * Rows<BF16, SRC, DP, QT, WQ, PARTS>::WAVES / 4))
 void rows_attention_kernel(RowsArgs a) {
   typedef Rows<BF16, SRC, DP, QT, WQ, PARTS> C;
   constexpr bool PAGED = C::PAGED, E4M3 = C::E4M3, VBF = C::VBF;
@@ -269,7 +270,7 @@ void rows_attention_kernel(RowsArgs a) {
   __shared__ __attribute__((aligned(16))) unsigned char lds[C::LDS_BYTES];
   __shared__ float scales[E4M3 ? 2 : 1][2][E4M3 ? KT : 1];
   __shared__ float merge_ml[NG == 1 ? 1 : 4][2][32];
-  __shared__ int strange[4];  // by wave: of a tile with rows that are not seen, some values are not finite
+  __shared__ int strange[C::WAVES];  // by wave: of a tile with rows that are not seen, some values are not finite
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, hl = lane >> 5;
@@ -322,16 +323,21 @@ void rows_attention_kernel(RowsArgs a) {
   const float c = a.scale_log2e;
 
   // staging: rows go from memory into LDS as they are, a wave's lanes side by side; what is exchanged is which chunk a lane
-  // loads.  This lane's row of a pass, its chunk of keys and of values
+  // loads.  This lane's row of a pass, its chunks of keys and of values
   const int srow = wave * C::RPW + lane / C::CPR;
-  const int kchunk = C::key_chunk(srow, lane % C::CPR), vchunk = C::value_chunk(srow, lane % C::CPR);
-  const bool k_in = kchunk * 16 < a.head_dim * C::EB, v_in = vchunk * 16 < a.head_dim * C::EB;
+  constexpr int TURNS = C::RPP % 16 ? 16 / C::RPP : 1;  // passes after which the keys' exchange is the same again
+  int kchunk[TURNS];
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) kchunk[i] = C::key_chunk(srow + i * C::RPP, lane % C::CPR);
+  const int vchunk = C::value_chunk(srow, lane % C::CPR);
+  const auto k_in = [&](int p) { return kchunk[p % TURNS] * 16 < a.head_dim * C::EB; };
+  const bool v_in = vchunk * 16 < a.head_dim * C::EB;
   // two buffers of keys and values
   const auto keys_of = [](int buf) { return buf * 2 * C::TILE_BYTES; };
   const auto values_of = [](int buf) { return buf * 2 * C::TILE_BYTES + C::TILE_BYTES; };
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)lds)) + wave * 1024;
   if (DP < C::PITCH || a.head_dim < DP) {  // what lies past head_dim is zero for good
-    for (int i = tid; i < 4 * C::TILE_BYTES / 16; i += kRowsThreads) reinterpret_cast<u32x4*>(lds)[i] = u32x4{};
+    for (int i = tid; i < 4 * C::TILE_BYTES / 16; i += C::THREADS) reinterpret_cast<u32x4*>(lds)[i] = u32x4{};
     __syncthreads();
   }
 
@@ -361,7 +367,7 @@ void rows_attention_kernel(RowsArgs a) {
   float ks = 0.0f, vs = 0.0f;  // scales of row tid of the unit requested
   // (the rows that a wave loads at once lie on one page: its address is the wave's)
   const bool page_wise = PAGED && a.pool.page_size % C::RPW == 0 && a.pool.kr < 1 << 26 && a.pool.vr < 1 << 26;
-  const uint32_t koff = uint32_t(lane / C::CPR) * uint32_t(PAGED ? a.pool.kr : a.kt) + kchunk * 16;
+  const uint32_t koff = uint32_t(lane / C::CPR) * uint32_t(PAGED ? a.pool.kr : a.kt);
   const uint32_t voff = uint32_t(lane / C::CPR) * uint32_t(PAGED ? a.pool.vr : a.vt) + vchunk * 16;
   const auto request = [&](int u, int buf) {
     const uint32_t lk = lds0 + keys_of(buf), lv = lds0 + values_of(buf);
@@ -371,12 +377,12 @@ void rows_attention_kernel(RowsArgs a) {
       const u32x4 rk = range_of(a.k + from * a.kt + int64_t(h) * a.kh, uint32_t((rows_here - 1) * a.kt) + a.head_dim * 2);
       const u32x4 rv = range_of(a.v + from * a.vt + int64_t(h) * a.vh, uint32_t((rows_here - 1) * a.vt) + a.head_dim * 2);
       const uint32_t kt = uint32_t(a.kt), vt = uint32_t(a.vt);
-      if (k_in)
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) to_lds(rk, koff, (p * C::RPP + wave * C::RPW) * kt, lk + p * 4096);
+      for (int p = 0; p < PASSES; ++p)
+        if (k_in(p)) to_lds(rk, koff + kchunk[p % TURNS] * 16, (p * C::RPP + wave * C::RPW) * kt, lk + p * (C::WAVES * 1024));
       if (v_in)
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) to_lds(rv, voff, (p * C::RPP + wave * C::RPW) * vt, lv + p * 4096);
+        for (int p = 0; p < PASSES; ++p) to_lds(rv, voff, (p * C::RPP + wave * C::RPW) * vt, lv + p * (C::WAVES * 1024));
     } else {
 #pragma unroll
       for (int i = 0; i < EN; ++i)
@@ -393,16 +399,16 @@ void rows_attention_kernel(RowsArgs a) {
           const Place at = place_of(first, e);
           const u32x4 rk = range_of(hk + at.page * a.pool.kp + at.in_page * a.pool.kr, 0x7fffffffu);
           const u32x4 rv = range_of(hv + at.page * a.pool.vp + at.in_page * a.pool.vr, 0x7fffffffu);
-          if (k_in) to_lds(rk, koff, 0, lk + p * 4096);
-          if (v_in) to_lds(rv, voff, 0, lv + p * 4096);
+          if (k_in(p)) to_lds(rk, koff + kchunk[p % TURNS] * 16, 0, lk + p * (C::WAVES * 1024));
+          if (v_in) to_lds(rv, voff, 0, lv + p * (C::WAVES * 1024));
         }
       } else {
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
           const int row = p * C::RPP + srow, key = u * KT + row < seq.m ? u * KT + row : seq.m - 1;
           const Place at = place_of(key, __shfl(entry[row >= 64 ? EN - 1 : 0], row & 63, 64));
-          if (k_in) to_lds(hk + at.page * a.pool.kp + at.in_page * a.pool.kr + kchunk * 16, lk + p * 4096);
-          if (v_in) to_lds(hv + at.page * a.pool.vp + at.in_page * a.pool.vr + vchunk * 16, lv + p * 4096);
+          if (k_in(p)) to_lds(hk + at.page * a.pool.kp + at.in_page * a.pool.kr + kchunk[p % TURNS] * 16, lk + p * (C::WAVES * 1024));
+          if (v_in) to_lds(hv + at.page * a.pool.vp + at.in_page * a.pool.vr + vchunk * 16, lv + p * (C::WAVES * 1024));
         }
       }
       if constexpr (E4M3) {
@@ -445,9 +451,10 @@ void rows_attention_kernel(RowsArgs a) {
   // two steps of 8-bit elements).  Values: see read_transposed; the rows of a lane's element j are 4 hl + j (j < 4) and
   // 4 hl + 8 + j - 4, which is how S^T's rows lie in registers
   constexpr int KB = C::KX / 2;
-  int kbase[KB], vbase[4];
+  constexpr bool EXCHANGE = DP > 192;  // (the widest rows leave no registers for the bases but the first)
+  int kbase[EXCHANGE ? 1 : KB], vbase[4];
 #pragma unroll
-  for (int j = 0; j < KB; ++j) kbase[j] = r * PB + C::key_chunk(r, 2 * j + hl) * 16;
+  for (int j = 0; j < (EXCHANGE ? 1 : KB); ++j) kbase[j] = r * PB + C::key_chunk(r, 2 * j + hl) * 16;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = lane & 15, g = lane >> 4 & 1;
@@ -461,7 +468,8 @@ void rows_attention_kernel(RowsArgs a) {
   }
   // (the exchanges stay among the chunks that the bases cover)
   const auto key_words = [&](const unsigned char* at, int j) {
-    return *reinterpret_cast<const u32x4*>(at + kbase[j % KB] + j / KB * 256);
+    const int base = EXCHANGE ? kbase[0] ^ j % KB * 32 : kbase[EXCHANGE ? 0 : j % KB];
+    return *reinterpret_cast<const u32x4*>(at + base + j / KB * 256);
   };
   const auto value_operand = [&](const unsigned char* at, int f) {
     if constexpr (E4M3) {
@@ -520,13 +528,16 @@ void rows_attention_kernel(RowsArgs a) {
       u32x4* const mine = reinterpret_cast<u32x4*>(lds + values_of(buf)) + tid;
       uint32_t bad = 0;
 #pragma unroll
-      for (int p = 0; p < C::TILE_BYTES / 16 / kRowsThreads; ++p)
+      for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= E4M3 ? nan_codes(mine[p * kRowsThreads][i]) : not_finite<BF16>(mine[p * kRowsThreads][i]);
+        for (int i = 0; i < 4; ++i) bad |= E4M3 ? nan_codes(mine[p * C::THREADS][i]) : not_finite<BF16>(mine[p * C::THREADS][i]);
       const bool any = __ballot(bad != 0) != 0;
       if (lane == 0) strange[wave] = any;
       __syncthreads();
-      if (strange[0] | strange[1] | strange[2] | strange[3]) {
+      int found = 0;
+#pragma unroll
+      for (int i = 0; i < C::WAVES; ++i) found |= strange[i];
+      if (found) {
 #pragma unroll 1
         for (int j = 0; j < 2 * NSUB; ++j) {
           const unsigned char* base = lds + values_of(buf) + (wg * NSUB * 2 + j) * 16 * PB;
@@ -562,11 +573,11 @@ void rows_attention_kernel(RowsArgs a) {
         }
         __syncthreads();
 #pragma unroll
-        for (int p = 0; p < C::TILE_BYTES / 16 / kRowsThreads; ++p) {
-          u32x4 w = mine[p * kRowsThreads];
+        for (int p = 0; p < PASSES; ++p) {
+          u32x4 w = mine[p * C::THREADS];
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] &= ~(E4M3 ? nan_codes(w[i]) : not_finite<BF16>(w[i]));
-          mine[p * kRowsThreads] = w;
+          mine[p * C::THREADS] = w;
         }
         __syncthreads();
       }
@@ -712,20 +723,22 @@ void rows_attention_kernel(RowsArgs a) {
     l[t] = y + z;
   }
   const bool whole = parts == 1;
+  // (a lane's place as if it were new: what follows from it is not kept in registers through the loop)
+  const int end_tid = fresh(int(threadIdx.x)), end_r = end_tid & 31, end_hl = end_tid >> 5 & 1;
   if constexpr (NG == 1) {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      const int local = (wq * QT + t) * 32 + r, row = row0 + local;
+      const int local = (wq * QT + t) * 32 + end_r, row = row0 + local;
       const bool real = row < rows;
       const int tok = int(udiv(uint32_t(real ? row : rows - 1), a.group_div)), g = (real ? row : rows - 1) - tok * a.group;
       if (!whole) {
         const int64_t slot = int64_t(blockIdx.x) * BM + local;
-        if (hl == 0) a.part_ml[2 * slot] = m[t], a.part_ml[2 * slot + 1] = l[t] * (1.0f / float(1 << C::RAISE));
+        if (end_hl == 0) a.part_ml[2 * slot] = m[t], a.part_ml[2 * slot + 1] = l[t] * (1.0f / float(1 << C::RAISE));
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int d = 32 * f + 8 * i + 4 * hl;
+            const int d = 32 * f + 8 * i + 4 * end_hl;
             if (d < a.head_dim) {
               f32x4 y;
 #pragma unroll
@@ -750,27 +763,27 @@ void rows_attention_kernel(RowsArgs a) {
               w[y][j] = pack2<BF16>(o[t][f][8 * i + 4 * y + 2 * j] * inv, o[t][f][8 * i + 4 * y + 2 * j + 1] * inv);
           const auto e0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
           const auto e1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-          const int d = 32 * f + 16 * i + 8 * hl;
+          const int d = 32 * f + 16 * i + 8 * end_hl;
           if (real && d < a.head_dim) *reinterpret_cast<u32x4*>(out + 2 * d) = u32x4{e0[0], e1[0], e0[1], e1[1]};
         }
-      if (a.lse && real && hl == 0)
+      if (a.lse && real && end_hl == 0)
         a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] =
             lse_of(m[t], l[t] * (1.0f / float(1 << C::RAISE)), a.scale);
     }
   } else {
     float* const mo = reinterpret_cast<float*>(lds);
     __syncthreads();  // the last tile has been read
-    if (hl == 0) merge_ml[wave][0][r] = m[0], merge_ml[wave][1][r] = l[0];
+    if (end_hl == 0) merge_ml[wave][0][end_r] = m[0], merge_ml[wave][1][end_r] = l[0];
 #pragma unroll
     for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4*>(mo + (wave * 32 + r) * C::OP + 32 * f + 8 * i + 4 * hl) =
+        *reinterpret_cast<f32x4*>(mo + (wave * 32 + end_r) * C::OP + 32 * f + 8 * i + 4 * end_hl) =
             f32x4{o[0][f][4 * i], o[0][f][4 * i + 1], o[0][f][4 * i + 2], o[0][f][4 * i + 3]};
     __syncthreads();
-    constexpr int LPR = C::PITCH / 4, AT_ONCE = kRowsThreads / LPR;  // lanes a row, rows at once
-    const int d = tid % LPR * 4;
-    for (int local = tid / LPR; local < BM; local += AT_ONCE) {
+    constexpr int LPR = C::PITCH / 4, AT_ONCE = C::THREADS / LPR;  // lanes a row, rows at once
+    const int d = end_tid % LPR * 4;
+    for (int local = end_tid / LPR; local < BM; local += AT_ONCE) {
       const int row = row0 + local;
       if (row >= rows || d >= a.head_dim) continue;
       const int w0 = local / 32, rr = local % 32;
