@@ -6,9 +6,11 @@ namespace dev {
 
 template <bool BF16, int DP>
 void prompt_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
-  if (shape.tile_rows == 64) return attend_rows<BF16, 0, DP, 1, 2, 1>(a, s);
-  if constexpr (DP > 128) return attend_rows<BF16, 0, DP, 1, 8, 1>(a, s);
-  else return attend_rows<BF16, 0, DP, 1, 4, 1>(a, s);
+  if constexpr (DP > 64)
+    if (shape.tile_rows == 256) return attend_rows<BF16, 0, DP, 8, 8, 1>(a, s);
+  if constexpr (DP > 128) return attend_rows<BF16, 0, DP, 4, 8, 1>(a, s);
+  else if (shape.tile_rows == 128) return attend_rows<BF16, 0, DP, 4, 4, 1>(a, s);
+  else return attend_rows<BF16, 0, DP, 2, 4, 1>(a, s);
 }
 
 template <bool BF16>

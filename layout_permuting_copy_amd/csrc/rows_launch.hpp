@@ -6,13 +6,14 @@
 namespace tc {
 namespace dev {
 
-template <bool BF16, int SRC, int DP, int QT, int WQ, int PARTS>
+template <bool BF16, int SRC, int DP, int WQ, int WAVES, int PARTS>
 void attend_rows(const RowsArgs& a, hipStream_t s) {
-  typedef Rows<BF16, SRC, DP, QT, WQ, PARTS> C;
-  hipLaunchKernelGGL((rows_attention_kernel<BF16, SRC, DP, QT, WQ, PARTS>), dim3(uint32_t(a.workgroups)), dim3(C::THREADS), 0, s, a);
-  if (a.slots)
-    hipLaunchKernelGGL((rows_join_kernel<BF16, C::PAGED, C::BM, C::KT>), dim3(uint32_t(a.tiles * a.heads * (C::BM / 4))),
-                       dim3(kRowsThreads), 0, s, a);
+  typedef Rows<BF16, SRC, DP, WQ, WAVES, PARTS> C;
+  hipLaunchKernelGGL((rows_attention_kernel<BF16, SRC, DP, WQ, WAVES, PARTS>), dim3(uint32_t(a.workgroups)), dim3(C::THREADS), 0, s, a);
+  if constexpr (C::PAGED)
+    if (a.slots)
+      hipLaunchKernelGGL((rows_join_kernel<BF16, true, DP, C::BM, C::KT>), dim3(uint32_t(a.tiles * a.heads * (C::BM / kJoinRows))),
+                         dim3(kRowsThreads), 0, s, a);
 }
 
 }  // namespace dev
