@@ -64,10 +64,10 @@ Queries queries_of(const void* q, const tc_layout* q_layout, void* out, const tc
 }
 
 void apart_from_inputs(const Operand* const* outs, int n_outs, Operands inputs) {
-  for (int i = 0; i < n_outs; ++i) {
-    for (const Operand* y : inputs) apart("an output and an input", *outs[i], *y);
+  for (int i = 0; i < n_outs; ++i)
     for (int j = 0; j < i; ++j) apart("two outputs", *outs[i], *outs[j]);
-  }
+  for (int i = 0; i < n_outs; ++i)
+    for (const Operand* y : inputs) apart("an output and an input", *outs[i], *y);
 }
 
 void dealt(tc::RowsArgs* a, const tc::RowsShape& shape, int64_t heads, int64_t group) {

@@ -695,6 +695,7 @@ void rows_attention_kernel(RowsArgs a) {
           }
         }
 
+      if constexpr (DP > 192) __builtin_amdgcn_sched_barrier(0);  // (one product's registers at a time)
       l = CHAINS == 1 ? sum[0] : (sum[0] + sum[1 % CHAINS]) + (sum[2 % CHAINS] + sum[3 % CHAINS]);
 
       if constexpr (EXCHANGE) bases = bases_of(fresh(int(threadIdx.x)) & 63);
