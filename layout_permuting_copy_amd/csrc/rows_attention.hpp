@@ -280,7 +280,8 @@ struct Rows {
   static constexpr int LDS_BYTES = 4 * TILE_BYTES > MEET_BYTES ? 4 * TILE_BYTES : MEET_BYTES;
   // Workgroups that a compute unit holds: eight waves, two a SIMD, that hide each other's waits.  (With one a SIMD and twice
   // the registers half of those are the matrix unit's own, and what has to be moved out of them and back costs more.)
-  static constexpr int RESIDENT = 8 / WAVES;
+  // Narrow heads of caches leave room for three (32 trees of 8 tokens, heads of 64: 68 -> 65 us).
+  static constexpr int RESIDENT = WAVES == 8 ? 1 : PAGED && DP == 64 ? 3 : 2;
   static_assert(RESIDENT * LDS_BYTES <= 150 * 1024, "they share 160 KB of LDS");
 
   // Which 16-byte chunk of a row lies at place c of its row in LDS, and the other way round (an exchange): the rows that one
@@ -461,6 +462,9 @@ void rows_attention_kernel(RowsArgs a) {
   // which is found anew for each product)
   constexpr int KB = C::KX / 2;
   constexpr bool EXCHANGE = DP > 192;
+  // 8-bit tiles of 32 rows are in registers, as codes, before the first product: their conversions do not wait for LDS (16
+  // trees of 12 tokens, 8 heads a group, over 8192 rows: 164 -> 133 us)
+  constexpr bool EARLY = E4M3 && DP <= 128;
   struct Bases {
     int k[EXCHANGE ? 1 : KB], v[EXCHANGE ? 1 : 4];
   };
@@ -486,10 +490,15 @@ void rows_attention_kernel(RowsArgs a) {
     const int base = EXCHANGE ? bases.k[0] ^ j % KB * 32 : bases.k[EXCHANGE ? 0 : j % KB];
     return *reinterpret_cast<const u32x4*>(at + base + j / KB * 256);
   };
+  const auto value_codes = [&](const unsigned char* at, int f) {
+    return read_transposed8(at + (EXCHANGE ? bases.v[0] ^ (f & 3) * 32 : bases.v[EXCHANGE ? 0 : f & 3]) + (f >> 2) * 128);
+  };
+  const auto values_of_codes = [](const u32x2& w) {
+    return u32x4{from_e4m3<true, false>(w[0]), from_e4m3<true, true>(w[0]), from_e4m3<true, false>(w[1]), from_e4m3<true, true>(w[1])};
+  };
   const auto value_operand = [&](const unsigned char* at, int f) {
     if constexpr (E4M3) {
-      const u32x2 w = read_transposed8(at + (EXCHANGE ? bases.v[0] ^ (f & 3) * 32 : bases.v[EXCHANGE ? 0 : f & 3]) + (f >> 2) * 128);
-      return u32x4{from_e4m3<true, false>(w[0]), from_e4m3<true, true>(w[0]), from_e4m3<true, false>(w[1]), from_e4m3<true, true>(w[1])};
+      return values_of_codes(value_codes(at, f));
     } else {
       const unsigned char* p = at + (EXCHANGE ? bases.v[0] ^ (f & 3) * 64 : bases.v[EXCHANGE ? 0 : f & 3]) + (f >> 2) * 256;
       const u32x2 lo = read_transposed(p), hi = read_transposed(p + 8 * PB);
@@ -598,14 +607,26 @@ void rows_attention_kernel(RowsArgs a) {
       if constexpr (EXCHANGE) bases = bases_of(fresh(int(threadIdx.x)) & 63);
       // S^T = K Q^T
       f32x16 s[NJ];
+      u32x2 codes[EARLY ? 2 : 1][EARLY ? NF : 1];
 #pragma unroll
       for (int n = 0; n < NJ; ++n) {
         const unsigned char* base = lds + keys_of(buf) + (wg * NSUB + n0 + n) * 32 * PB;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
+        u32x4 early[EARLY ? KS / 2 : 1];
+        if constexpr (EARLY) {
+#pragma unroll
+          for (int j = 0; j < KS / 2; ++j) early[j] = key_words(base, j);
+          const unsigned char* values = lds + values_of(buf) + (wg * NSUB + n0 + n) * 32 * PB;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int f = 0; f < NF; ++f) codes[k][f] = value_codes(values + 16 * k * PB, f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int j = 0; j < (E4M3 ? KS / 2 : KS); ++j) {
-          const u32x4 w = key_words(base, j);
+          const u32x4 w = EARLY ? early[EARLY ? j : 0] : key_words(base, j);
 #pragma unroll
           for (int half = 0; half < (E4M3 ? 2 : 1); ++half) {
             u32x4 y = w;
@@ -669,20 +690,33 @@ void rows_attention_kernel(RowsArgs a) {
       ref = finite(ref);
       constexpr int CHAINS = DP > 128 ? 1 : 4;  // of additions
       float sum[CHAINS] = {l};
+      const auto weight = [&](int n, int i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, -ref)) * float(1 << C::RAISE);
+        sum[i % CHAINS] += e;
+        return e;
+      };
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&scales[buf][1][(wg * NSUB + n0 + n) * 32 + 2 * i + 4 * hl]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[n][i + j] = weight(n, i + j) * x[j];
+          }
+          if (now_edge) {  // (0 times a scale that is no number)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[n][i] = seen_of(n) >> (8 * (i / 4) + i % 4) & 1 ? s[n][i] : 0.0f;
+          }
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NJ; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * k + i], c, -ref)) * float(1 << C::RAISE);
-            sum[i % CHAINS] += e[i];
-            if constexpr (E4M3) {
-              e[i] *= scales[buf][1][(wg * NSUB + n0 + n) * 32 + 16 * k + 8 * (i / 4) + 4 * hl + i % 4];
-              if (now_edge) e[i] = seen_of(n) >> (16 * k + 8 * (i / 4) + i % 4) & 1 ? e[i] : 0.0f;
-            }
-          }
+          for (int i = 0; i < 8; ++i) e[i] = E4M3 ? s[n][8 * k + i] : weight(n, 8 * k + i);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float x = e[2 * i], y = e[2 * i + 1];
@@ -707,7 +741,7 @@ void rows_attention_kernel(RowsArgs a) {
           const unsigned char* base = lds + values_of(buf) + ((wg * NSUB + n0 + n) * 32 + 16 * k) * PB;
 #pragma unroll
           for (int f = 0; f < NF; ++f) {
-            const u32x4 y = value_operand(base, f);
+            const u32x4 y = EARLY ? values_of_codes(codes[EARLY ? k : 0][EARLY ? f : 0]) : value_operand(base, f);
 #pragma unroll
             for (int z = 0; z < PARTS; ++z) o[f] = mfma32<VBF>(y, p[n][k][z], o[f]);
           }

@@ -8,8 +8,8 @@ namespace tc {
 namespace {
 
 constexpr int64_t kCus = 256;
-// Workgroups that a compute unit holds: two of four waves, one of eight.
-int64_t resident(int64_t head_dim) { return head_dim > 128 ? 1 : 2; }
+// Workgroups that a compute unit holds: of heads above 128 elements one of eight waves, else two of four, or three.
+int64_t resident(int64_t head_dim) { return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 3; }
 int64_t least_tile(int64_t head_dim) { return head_dim > 128 ? 128 : 64; }
 int64_t tiles_of(int64_t rows, int64_t batch, int64_t tile) { return std::min(rows, rows / tile + batch); }
 
