@@ -102,6 +102,7 @@ struct RowsArgs {
   const int64_t* masks;  // or NULL: a token sees the rows up to its own, where causal
   float* part_o;         // [workgroups][tile rows][head_dim]: a part's sum of p v, relative to its maximum
   float* part_ml;        // [workgroups][tile rows][2]: its maximum (of q k) and sum
+  uint32_t* part_units;  // units that a part has at most, before all of these
   int32_t batch, tokens, key_rows, heads, group, head_dim, max_len, causal;
   int32_t slots, least;  // workgroups that the parts of tiles should fill (0: tiles are whole), units a part has at least
   int64_t tiles, workgroups;  // at most: tiles of all sequences, workgroups of the call
@@ -159,6 +160,7 @@ int64_t paged_logit_row(int64_t max_len);
 struct RowsShape {
   int64_t tile_rows, unit_rows, tiles, slots, least, workgroups;
 };
+constexpr int64_t kRowsWorkspaceHead = 256;  // bytes: a number, and the parts on lines of their own
 RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 // Bytes that suffice for the parts of tiles at these sizes and at any smaller batch, tokens and max_len.
 int64_t rows_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);

@@ -165,7 +165,7 @@ int tc_paged_tree_attention(const tc_paged_cache* cache, const void* q, const tc
     }
     if (c.q.empty || batch == 0) return TC_OK;
     const tc::RowsShape shape = tc::rows_shape(true, batch, tokens, p.heads, group, p.dim, max_len);
-    const int64_t slots = shape.slots ? shape.workgroups * shape.tile_rows : 0, bytes = slots * (p.dim + 2) * 4;
+    const int64_t slots = shape.slots ? shape.workgroups * shape.tile_rows : 0, bytes = slots ? tc::kRowsWorkspaceHead + slots * (p.dim + 2) * 4 : 0;
     need(workspace_bytes >= bytes, TC_E_ARG, "workspace too small");
     need(workspace || bytes == 0, TC_E_NULL, "null workspace");
     need(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, TC_E_ALIGN, "workspace not aligned to 16 bytes");
@@ -181,7 +181,8 @@ int tc_paged_tree_attention(const tc_paged_cache* cache, const void* q, const tc
     a.lens = reinterpret_cast<const int32_t*>(lens.p);
     a.starts = reinterpret_cast<const int32_t*>(starts.p);
     a.masks = masks ? reinterpret_cast<const int64_t*>(mo.p) : nullptr;
-    a.part_o = static_cast<float*>(workspace);
+    a.part_units = static_cast<uint32_t*>(workspace);
+    a.part_o = static_cast<float*>(workspace) + tc::kRowsWorkspaceHead / 4;
     a.part_ml = a.part_o + slots * p.dim;
     a.batch = int32_t(batch);
     a.causal = 1;

@@ -155,6 +155,8 @@ struct RowsWalk {
     }
     return sum;
   }
+  // SEARCH: finds `most`, else it is what the workgroups of the attention found
+  template <bool SEARCH>
   __device__ __forceinline__ void init(const RowsArgs& a) {
     const int lane = threadIdx.x & 63;
     per = (a.batch + 63) / 64;
@@ -162,6 +164,10 @@ struct RowsWalk {
     if (per == 1 && lane < a.batch) mine = rows_seq<PAGED>(a, lane);
     most = 1;
     if (!a.slots) return;
+    if constexpr (!SEARCH) {
+      most = uint32_t(__builtin_amdgcn_readfirstlane(int(*a.part_units)));
+      return;
+    }
     uint32_t sum = 0, longest = 1;
     float work = 0.0f;
     for (int k = 0; k < per && lane * per + k < a.batch; ++k) {
@@ -317,7 +323,8 @@ void rows_attention_kernel(RowsArgs a) {
   const int h = int(blockIdx.x - x * a.heads_div.d);
 
   RowsWalk<PAGED, BM, KT> walk;
-  walk.init(a);
+  walk.template init<true>(a);
+  if (PAGED && a.slots && blockIdx.x == 0 && tid == 0) *a.part_units = walk.most;
   int b;
   uint32_t at, first;
   RowsSeq seq;
@@ -336,10 +343,10 @@ void rows_attention_kernel(RowsArgs a) {
   const int each = parts > 1 ? (int(walk.units(seq)) + parts - 1) / parts : units_all;
   const int u0 = part * each, u1 = u0 + each < units_all ? u0 + each : units_all;
 
-  // this lane's query row
+  // this lane's query row (what was loaded is put right below, when the first keys and values are on their way)
   const int wq = wave % WQ, wg = wave / WQ;
   u32x4 q[KS];
-  {
+  const auto load_queries = [&] {
     const int row = row0 + wq * 32 + r;
     const uint32_t rr = uint32_t(row < rows ? row : rows - 1);
     const int tok = int(udiv(rr, a.group_div)), g = int(rr) - tok * a.group;
@@ -347,12 +354,9 @@ void rows_attention_kernel(RowsArgs a) {
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const int e = C::q_element(k, hl);
-      const bool in = e < a.head_dim;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(at + (in ? 2 * e : 0));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[k][i] = in ? (w[i] & a.q_and) ^ a.q_xor : 0u;
+      q[k] = *reinterpret_cast<const u32x4*>(at + (e < a.head_dim ? 2 * e : 0));
     }
-  }
+  };
   const float c = a.scale_log2e;
 
   // two buffers of keys and values
@@ -509,9 +513,14 @@ void rows_attention_kernel(RowsArgs a) {
   bool edge = false;  // of the tile to be computed
   if (u0 < u1) {
     load_entry(u0);
+    load_queries();
     request(u0, 0);
     edge = edge_of(u0);
     if (u0 + 1 < u1) load_entry(u0 + 1);
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[k][i] = C::q_element(k, hl) < a.head_dim ? (q[k][i] & a.q_and) ^ a.q_xor : 0u;
     settle();
   }
 #pragma unroll 1
@@ -842,61 +851,92 @@ void rows_attention_kernel(RowsArgs a) {
 constexpr int kJoinRows = 16;
 template <bool BF16, bool PAGED, int DP, int BM, int KT>
 __global__ __launch_bounds__(kRowsThreads) void rows_join_kernel(RowsArgs a) {
-  constexpr int LPR = DP <= 128 ? 32 : 64, AT_ONCE = kRowsThreads / LPR, CHUNKS = BM / kJoinRows;
+  constexpr int LPR = DP <= 128 ? 32 : 64, AT_ONCE = kRowsThreads / LPR, CHUNKS = BM / kJoinRows, MINE = kJoinRows / AT_ONCE;
   const int lane = threadIdx.x % LPR;
   RowsWalk<PAGED, BM, KT> walk;
-  walk.init(a);
+  walk.template init<false>(a);
   const uint32_t chunk = blockIdx.x % CHUNKS, y = blockIdx.x / CHUNKS, x = udiv(y, a.heads_div);
   const int h = int(y - x * a.heads_div.d);
   int b;
   uint32_t tile, first;
   RowsSeq seq;
   if (!walk.template find<false, false>(a, x, &b, &tile, &first, &seq)) return;
-  const int parts = int(walk.parts(a, seq)), tiles = int(walk.tiles(a, seq));
-  if (parts == 1) return;
+  const int parts = int(walk.parts(a, seq)), tiles = int(walk.tiles(a, seq)), rows = seq.n * a.group;
+  const int row0 = int(tile) * BM + int(chunk) * kJoinRows;
+  if (parts == 1 || row0 >= rows) return;
   // part k's rows are those of workgroup (first + k * tiles + tile) * heads + h
-  const int64_t step = int64_t(tiles) * a.heads * BM;
-  for (int i = int(threadIdx.x) / LPR; i < kJoinRows; i += AT_ONCE) {
-    const int local = int(chunk) * kJoinRows + i, row = int(tile) * BM + local;
-    if (row >= seq.n * a.group) continue;
-    const int64_t slot = (int64_t(first + tile) * a.heads + h) * BM + local;
-    float top = -kInf;
-    for (int k = lane; k < parts; k += LPR) top = __builtin_fmaxf(top, a.part_ml[2 * (slot + k * step)]);
+  const int64_t step = int64_t(tiles) * a.heads * BM, slot0 = (int64_t(first + tile) * a.heads + h) * BM + chunk * kJoinRows;
+  const int d0 = 4 * lane < a.head_dim ? 4 * lane : 0;
+  // a lane's MINE rows side by side; past the last row, that one again
+  const float* ml[MINE];
+  const float* from[MINE];
+  f32x4 all[MINE];
+  float top[MINE], total[MINE], m[MINE], l[MINE];
+  constexpr int AHEAD = 4;  // parts requested at once
+  f32x4 v[MINE][AHEAD];
 #pragma unroll
-    for (int d = 1; d < LPR; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d, LPR));
-    const float ref = finite(top);
-    const int d0 = 4 * lane < a.head_dim ? 4 * lane : 0;
-    f32x4 all = {0.0f, 0.0f, 0.0f, 0.0f};
-    float total = 0.0f;
-    for (int k0 = 0; k0 < parts; k0 += LPR) {
-      const int here = parts - k0 < LPR ? parts - k0 : LPR;
-      float f = 0.0f;
-      if (lane < here) {
-        const float* ml = a.part_ml + 2 * (slot + (k0 + lane) * step);
-        f = __builtin_amdgcn_exp2f((ml[0] - ref) * a.scale_log2e);
-        total += ml[1] * f;
+  for (int z = 0; z < MINE; ++z) {
+    const int i = int(threadIdx.x) / LPR + z * AT_ONCE;
+    const int64_t slot = slot0 + (row0 + i < rows ? i : rows - 1 - row0);
+    ml[z] = a.part_ml + 2 * slot;
+    from[z] = a.part_o + slot * a.head_dim + d0;
+    const float* at = ml[z] + 2 * (lane < parts ? lane : 0) * step;
+    m[z] = at[0], l[z] = at[1];
+  }
+  const auto request = [&](int k0) {
+#pragma unroll
+    for (int z = 0; z < MINE; ++z)
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+        v[z][j] = *reinterpret_cast<const f32x4*>(from[z] + (k0 + j < parts ? k0 + j : parts - 1) * step * a.head_dim);
+  };
+  request(0);
+#pragma unroll
+  for (int z = 0; z < MINE; ++z) {
+    if (lane >= parts) m[z] = -kInf;
+    top[z] = m[z];
+    for (int k = lane + LPR; k < parts; k += LPR) top[z] = __builtin_fmaxf(top[z], ml[z][2 * k * step]);
+#pragma unroll
+    for (int d = 1; d < LPR; d *= 2) top[z] = __builtin_fmaxf(top[z], __shfl_xor(top[z], d, LPR));
+    all[z] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    total[z] = 0.0f;
+  }
+  for (int k0 = 0; k0 < parts; k0 += LPR) {
+    float f[MINE];  // of part k0 + lane
+#pragma unroll
+    for (int z = 0; z < MINE; ++z) {
+      if (k0) {
+        const float* at = ml[z] + 2 * (k0 + lane < parts ? k0 + lane : 0) * step;
+        m[z] = k0 + lane < parts ? at[0] : -kInf, l[z] = at[1];
       }
-      const float* from = a.part_o + (slot + k0 * step) * a.head_dim + d0;
-      int k = 0;
-      for (; k + 4 <= here; k += 4) {
-        f32x4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const f32x4*>(from + (k + j) * step * a.head_dim);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) all += v[j] * __shfl(f, k + j, LPR);
-      }
-      for (; k < here; ++k) all += *reinterpret_cast<const f32x4*>(from + k * step * a.head_dim) * __shfl(f, k, LPR);
+      f[z] = k0 + lane < parts ? __builtin_amdgcn_exp2f((m[z] - finite(top[z])) * a.scale_log2e) : 0.0f;
+      if (k0 + lane < parts) total[z] += l[z] * f[z];
     }
+    for (int k = k0; k < parts && k < k0 + LPR; k += AHEAD) {
+      if (k) request(k);
 #pragma unroll
-    for (int d = 1; d < LPR; d *= 2) total += __shfl_xor(total, d, LPR);
+      for (int z = 0; z < MINE; ++z)
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const float g = __shfl(f[z], k - k0 + j, LPR);
+          if (k + j < parts) all[z] += v[z][j] * g;
+        }
+    }
+  }
+#pragma unroll
+  for (int z = 0; z < MINE; ++z) {
+#pragma unroll
+    for (int d = 1; d < LPR; d *= 2) total[z] += __shfl_xor(total[z], d, LPR);
+    const int row = row0 + int(threadIdx.x) / LPR + z * AT_ONCE;
+    if (row >= rows) continue;
     const int tok = int(udiv(uint32_t(row), a.group_div)), g = row - tok * a.group;
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float inv = total[z] == 0.0f ? 0.0f : 1.0f / total[z];
     if (4 * lane < a.head_dim) {
       unsigned char* out = a.out + int64_t(seq.t0 + tok) * a.ot + (int64_t(h) * a.group + g) * a.oh;
-      *reinterpret_cast<u32x2*>(out + 8 * lane) = u32x2{pack2<BF16>(all[0] * inv, all[1] * inv), pack2<BF16>(all[2] * inv, all[3] * inv)};
+      *reinterpret_cast<u32x2*>(out + 8 * lane) = u32x2{pack2<BF16>(all[z][0] * inv, all[z][1] * inv), pack2<BF16>(all[z][2] * inv, all[z][3] * inv)};
     }
     if (a.lse && lane == 0)
-      a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] = lse_of(top, total, a.scale);
+      a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] = lse_of(top[z], total[z], a.scale);
   }
 }
 

@@ -52,7 +52,7 @@ int64_t rows_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t gro
   for (int64_t tile = least_tile(head_dim); tile <= 128; tile *= 2) {
     const int64_t fill = kCus * resident(head_dim);
     const int64_t workgroups = (std::min(tiles_of(tokens * group, batch, tile) * heads, 2 * fill) + fill - 1) / fill * fill;
-    most = std::max(most, workgroups * tile * (head_dim + 2) * 4);
+    most = std::max(most, kRowsWorkspaceHead + workgroups * tile * (head_dim + 2) * 4);
   }
   return tokens * group == 0 || batch == 0 ? 0 : most;
 }
