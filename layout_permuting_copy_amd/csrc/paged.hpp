@@ -161,7 +161,7 @@ struct RowsShape {
   int64_t tile_rows, unit_rows, tiles, slots, least, workgroups;
 };
 constexpr int64_t kRowsWorkspaceHead = 256;  // bytes: a number, and the parts on lines of their own
-RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
+RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 // Bytes that suffice for the parts of tiles at these sizes and at any smaller batch, tokens and max_len.
 int64_t rows_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 

@@ -122,7 +122,7 @@ int tc_prompt_attention(const void* q, const tc_layout* q_layout, const void* k,
     a.key_rows = int32_t(ko.empty ? 0 : rows);
     a.batch = int32_t(batch);
     a.causal = causal;
-    const tc::RowsShape shape = tc::rows_shape(false, batch, tokens, heads, q_heads / heads, dim, 0);
+    const tc::RowsShape shape = tc::rows_shape(false, false, batch, tokens, heads, q_heads / heads, dim, 0);
     dealt(&a, shape, heads, q_heads / heads);
     return launched(tc::launch_prompt_attention(a, shape, dtype, stream));
   });
@@ -164,7 +164,7 @@ int tc_paged_tree_attention(const tc_paged_cache* cache, const void* q, const tc
       mo = operand("masks", masks, &l, 1, 8);
     }
     if (c.q.empty || batch == 0) return TC_OK;
-    const tc::RowsShape shape = tc::rows_shape(true, batch, tokens, p.heads, group, p.dim, max_len);
+    const tc::RowsShape shape = tc::rows_shape(true, p.dtype == TC_E4M3, batch, tokens, p.heads, group, p.dim, max_len);
     const int64_t slots = shape.slots ? shape.workgroups * shape.tile_rows : 0, bytes = slots ? tc::kRowsWorkspaceHead + slots * (p.dim + 2) * 4 : 0;
     need(workspace_bytes >= bytes, TC_E_ARG, "workspace too small");
     need(workspace || bytes == 0, TC_E_NULL, "null workspace");

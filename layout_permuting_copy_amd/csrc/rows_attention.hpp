@@ -66,6 +66,11 @@ __device__ __forceinline__ void to_lds(const float* p, uint32_t lds) {
 }
 __device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+__device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
+  return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(x >> 32), lane))) << 32 |
+                 uint32_t(__builtin_amdgcn_readlane(int(x), lane)));
+}
+
 // Whether any lane's is true, as a number that all have.
 __device__ __forceinline__ uint32_t any_lane(bool x) {
   const uint64_t lanes = __ballot(x);
@@ -413,15 +418,15 @@ void rows_attention_kernel(RowsArgs a) {
       const unsigned char* const hk = a.pool.k + int64_t(h) * a.pool.kh;
       const unsigned char* const hv = a.pool.v + int64_t(h) * a.pool.vh;
       if (page_wise) {
-        // (rows past the end lie on the last row's page all the same, as far as the wave's do)
+        // Lane i finds where row i lies (past the end: the last rows that a wave loads at once), the wave's rows are a lane's.
+        const int key = u * KT + lane < seq.m ? u * KT + lane : (seq.m - 1) & ~(C::RPW - 1);
+        const Place at = place_of(key, entry);
+        const int64_t k_at = at.page * a.pool.kp + at.in_page * a.pool.kr, v_at = at.page * a.pool.vp + at.in_page * a.pool.vr;
         const uint32_t ko = up * uint32_t(a.pool.kr) + kc, vo = up * uint32_t(a.pool.vr) + vc;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
           const int row = p * C::RPP + wave * C::RPW;
-          const int first = u * KT + row < seq.m ? u * KT + row : (seq.m - 1) / C::RPW * C::RPW;
-          const Place at = place_of(first, __builtin_amdgcn_readlane(entry, row));
-          const u32x4 rk = range_of(hk + at.page * a.pool.kp + at.in_page * a.pool.kr, 0x7fffffffu);
-          const u32x4 rv = range_of(hv + at.page * a.pool.vp + at.in_page * a.pool.vr, 0x7fffffffu);
+          const u32x4 rk = range_of(hk + lane_of(k_at, row), 0x7fffffffu), rv = range_of(hv + lane_of(v_at, row), 0x7fffffffu);
           if (k_in) to_lds(rk, ko, 0, lk + p * C::PASS_BYTES);
           if (v_in) to_lds(rv, vo, 0, lv + p * C::PASS_BYTES);
         }

@@ -8,14 +8,14 @@ namespace tc {
 namespace {
 
 constexpr int64_t kCus = 256;
-// Workgroups that a compute unit holds: of heads above 128 elements one of eight waves, else two of four, or three.
-int64_t resident(int64_t head_dim) { return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 3; }
+// Workgroups that a compute unit holds: one of eight waves (heads above 128 elements, tiles of 256 rows), else two of four, or three.
+int64_t resident(int64_t head_dim, int64_t tile) { return head_dim > 128 || tile == 256 ? 1 : head_dim > 64 ? 2 : 3; }
 int64_t least_tile(int64_t head_dim) { return head_dim > 128 ? 128 : 64; }
 int64_t tiles_of(int64_t rows, int64_t batch, int64_t tile) { return std::min(rows, rows / tile + batch); }
 
 }  // namespace
 
-RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len) {
+RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len) {
   RowsShape c{};
   const int64_t rows = tokens * group;
   if (paged) {
@@ -24,6 +24,10 @@ RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, i
     // from there down (16 trees of 64 rows over 8-bit caches: 112 us, in tiles of 128 rows 160).
     c.tile_rows = least_tile(head_dim);
     while (c.tile_rows < 128 && c.tile_rows * batch < 2 * rows) c.tile_rows *= 2;
+    // ... and of 256, by eight waves, once they are full (trees of 64 tokens, 8 heads a group, over 65536 rows: 356 -> 312 us;
+    // chunks of 1024 tokens over 16384: 636 -> 566; of 300, heads of 256: 355 -> 284).  Not of narrow heads, as of
+    // prompts, nor of wide 8-bit ones, for which the registers do not suffice.
+    if (head_dim > 64 && !(codes && head_dim > 128) && rows >= 256 * batch) c.tile_rows = 256;
   } else {
     // Larger tiles load their keys and values less often, smaller ones end more evenly: tiles of 128 rows once they are four a
     // compute unit (1024 tokens, 32 heads of 128 over 8: 42 us, in tiles of 64 rows 27; 4096 tokens 164 and 174), of 256 once
@@ -36,10 +40,10 @@ RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, i
   c.unit_rows = 64;
   c.tiles = tiles_of(rows, batch, c.tile_rows);
   c.workgroups = c.tiles * heads;
-  const int64_t fill = kCus * resident(head_dim);
+  const int64_t fill = kCus * resident(head_dim, c.tile_rows);
   if (paged && c.workgroups < 2 * fill && max_len > 512) {
     c.slots = fill;
-    c.least = 256 / c.unit_rows;
+    c.least = 2;  // (one tree of 8 tokens over 523 rows: 16.7 us, at least 4 units a part 18.6, one 17.1)
     // all parts fit the least multiple of `fill` that the tiles do
     c.workgroups = (c.workgroups + fill - 1) / fill * fill;
   }
@@ -49,8 +53,8 @@ RowsShape rows_shape(bool paged, int64_t batch, int64_t tokens, int64_t heads, i
 int64_t rows_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len) {
   if (max_len <= 512) return 0;
   int64_t most = 0;
-  for (int64_t tile = least_tile(head_dim); tile <= 128; tile *= 2) {
-    const int64_t fill = kCus * resident(head_dim);
+  for (int64_t tile = least_tile(head_dim); tile <= 256; tile *= 2) {
+    const int64_t fill = kCus * resident(head_dim, tile);
     const int64_t workgroups = (std::min(tiles_of(tokens * group, batch, tile) * heads, 2 * fill) + fill - 1) / fill * fill;
     most = std::max(most, kRowsWorkspaceHead + workgroups * tile * (head_dim + 2) * 4);
   }

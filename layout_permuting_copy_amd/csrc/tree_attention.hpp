@@ -8,6 +8,8 @@ namespace dev {
 
 template <bool BF16, int SRC, int DP, int PARTS>
 void tree_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
+  if constexpr (DP > 64 && !(SRC == 2 && DP > 128))
+    if (shape.tile_rows == 256) return attend_rows<BF16, SRC, DP, 8, 8, 1>(a, s);
   if constexpr (DP > 128) return attend_rows<BF16, SRC, DP, 4, 8, 1>(a, s);
   else if (shape.tile_rows == 64) return attend_rows<BF16, SRC, DP, 2, 4, PARTS>(a, s);
   else return attend_rows<BF16, SRC, DP, 4, 4, 1>(a, s);
