@@ -578,3 +578,43 @@ def test_empty_calls():
     out.fill_(7.0)
     L.tc_paged_tree_attention(e(2, 4, 64, **h), none, table, _i32([5, 6]), _i32([0, 1, 2]), out=out[:2])
     assert bool((out[:2] == 0).all()) and bool((out[2] == 7.0).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [80, 128, 144, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_in_the_largest_tiles(kind, dim, causal):
+    """Enough rows and heads for tiles of 256 rows; all heads are copies of two, and equal to them."""
+    n, heads = [2900, 1200], 32
+    gen = torch.Generator().manual_seed(dim)
+    q, k, v = _qkv(gen, P.DT[kind], sum(n), sum(n), 2, 1, dim)
+    which = torch.arange(heads) % 2
+    starts = _i32(R.starts_of(n))
+    out = L.tc_prompt_attention(q.cuda()[:, which], k.cuda()[:, which], v.cuda()[:, which], starts, causal=causal)
+    ref = _prompt_ref(q, k, v, n, n, causal)
+    for h in (0, 1):
+        R.close(out[:, h], ref[0][:, h], ref[2][:, h], "out", q.dtype)
+        assert torch.equal(out[:, h::2], out[:, h:h + 1].expand(-1, heads // 2, -1))
+
+
+LARGE = [  # heads, group, dim, page, major, lens, tokens (causal chunks)
+    (2, 1, 128, 24, "rows", [900, 300], [400, 257]), (1, 2, 96, 5, "heads", [513, 700], [130, 300]),
+    (1, 4, 256, 16, "rows", [600], [90]), (1, 2, 192, 7, "pairs", [300, 1400], [300, 129]), (2, 4, 128, 64, "heads", [640], [64])]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "bf16-e4m3", "fp16-e4m3"])
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s[:4])))
+def test_tree_in_the_largest_tiles(kind, shape):
+    """Sequences of 256 query rows and more, one page of each missing: chunks of prompts, and with masks."""
+    heads, group, dim, page, major, lens, n = shape
+    kinds = kind.split("-")
+    gen = torch.Generator().manual_seed(dim + page)
+    table, pages = P.table_for(lens, page, gen, spare=1)
+    for b, m in enumerate(lens):
+        table[b, (m // 2) // page] = -1
+    pool = P.Pool(kinds[-1], pages, page, heads, dim, major, gen)
+    q = torch.randn(sum(n), heads * group, dim, generator=gen).to(P.DT[kinds[0]])
+    say(f"[gpu] {n} tokens over {lens} rows")
+    _tree(q, pool, table, lens, n, page)
+    words = [w for t in n for w in _random_masks(gen, t, "any")]
+    _tree(q, pool, table, lens, n, page, words)
