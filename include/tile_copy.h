@@ -509,13 +509,18 @@ int64_t tc_paged_tree_attention_workspace(int64_t batch, int64_t tokens, int64_t
  * Tokens token_starts[b] .. token_starts[b + 1] - 1 (batch + 1 entries, contiguous, ascending, on the device) are sequence b, keys
  * key_starts[b] .. likewise (NULL: token_starts, keys == tokens).  With causal = 1 token i of n sees keys 0 .. m - n + i of m (its
  * sequence's last token all of them; none where that is below 0), with 0 all m.  x, lse, out, their precision (weights as one value) and
- * what becomes of rows that are not seen, of padding and of infinities are those of tc_paged_tree_attention.
+ * what becomes of rows that are not seen, of padding and of infinities are those of tc_paged_tree_attention, and so is the
+ * workspace, of tc_prompt_attention_workspace(...) bytes at the call's own sizes (0 unless there are few queries for long keys).
  * Errors: as above.
  */
 int tc_prompt_attention(const void* q, const tc_layout* q_layout, const void* k, const tc_layout* k_layout, const void* v,
                         const tc_layout* v_layout, void* out, const tc_layout* out_layout, int dtype, int64_t batch,
                         const int32_t* token_starts, const int32_t* key_starts, int causal, float scale, float* lse,
-                        const tc_layout* lse_layout, void* stream);
+                        const tc_layout* lse_layout, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tc_prompt_attention takes (0: none), or a negative status; keys: those of all sequences.  Host only. */
+int64_t tc_prompt_attention_workspace(int64_t batch, int64_t tokens, int64_t keys, int64_t q_heads, int64_t heads, int64_t head_dim);
+
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int tc_version(void);

@@ -170,8 +170,11 @@ def load_library(path: str = LIB_PATH):
     lib.tc_paged_evict.restype = ctypes.c_int
     lib.tc_paged_resize.argtypes = [vp, lp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
     lib.tc_paged_resize.restype = ctypes.c_int
-    lib.tc_prompt_attention.argtypes = [vp, lp, vp, lp, vp, lp, vp, lp, i32, i64, vp, vp, i32, ctypes.c_float, vp, lp, vp]
+    lib.tc_prompt_attention.argtypes = [vp, lp, vp, lp, vp, lp, vp, lp, i32, i64, vp, vp, i32, ctypes.c_float, vp, lp, vp, i64,
+                                        vp]
     lib.tc_prompt_attention.restype = ctypes.c_int
+    lib.tc_prompt_attention_workspace.argtypes = [i64] * 6
+    lib.tc_prompt_attention_workspace.restype = i64
     lib.tc_paged_tree_attention_workspace.argtypes = [i64] * 6
     lib.tc_paged_tree_attention_workspace.restype = ctypes.c_int64
     lib.tc_paged_tree_attention.argtypes = [vp, vp, lp, vp, lp, i32, vp, lp, vp, vp, vp, i64, ctypes.c_float, vp, lp, vp, i64, vp]
@@ -722,6 +725,21 @@ def tc_paged_resize(block_table, seq_lens, change, free_pages, free_count, page_
     return lens_out
 
 
+_rows_workspace_cache = {}
+
+
+def _workspace_bytes(entry, sizes):
+    need = _rows_workspace_cache.get((entry, sizes))
+    if need is None:
+        need = getattr(_lib, entry)(*sizes)
+        if need < 0:
+            _check(need)
+        if len(_rows_workspace_cache) >= 4096:
+            _rows_workspace_cache.clear()
+        _rows_workspace_cache[entry, sizes] = need
+    return need
+
+
 def tc_prompt_attention(q, k, v, token_starts, key_starts=None, causal: bool = True, scale: Optional[float] = None, out=None,
                         lse=None, stream=None):
     """Attention of packed sequences, ``q`` (tokens, q_heads, head_dim) over ``k``, ``v`` (keys, heads, head_dim), float16 or
@@ -760,17 +778,18 @@ def tc_prompt_attention(q, k, v, token_starts, key_starts=None, causal: bool = T
         elif out.dtype != q.dtype:
             raise ValueError(f"out is {out.dtype}, q {q.dtype}")
         ol = _lay(out)
+        key = (batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1] if k.dim() == 3 else 0, q.shape[2])
+        need = _workspace_bytes("tc_prompt_attention_workspace", key)
+        work = _empty_on(handle, dev, need, _torch.uint8) if need else None
         rc = lib.tc_prompt_attention(q.data_ptr(), ql[0], k.data_ptr(), kl[0], v.data_ptr(), vl[0], out.data_ptr(), ol[0], code, batch,
-                                     starts, key_at, 1 if causal else 0, scale, lp, ll[0], handle)
+                                     starts, key_at, 1 if causal else 0, scale, lp, ll[0], None if work is None else work.data_ptr(),
+                                     need, handle)
     finally:
         if back is not None:
             _torch.cuda.set_device(back)
     if rc != TC_OK:
         _check(rc)
     return out
-
-
-_tree_workspace_cache = {}
 
 
 def tc_paged_tree_attention(q, cache: PagedCache, block_table, seq_lens, token_starts, masks=None, scale: Optional[float] = None,
@@ -813,15 +832,7 @@ def tc_paged_tree_attention(q, cache: PagedCache, block_table, seq_lens, token_s
         elif out.dtype != q.dtype:
             raise ValueError(f"out is {out.dtype}, q {q.dtype}")
         ol = _lay(out)
-        key = (batch, tokens, q_heads, cache.heads, dim, max_len)
-        need = _tree_workspace_cache.get(key)
-        if need is None:
-            need = lib.tc_paged_tree_attention_workspace(*key)
-            if need < 0:
-                _check(need)
-            if len(_tree_workspace_cache) >= 4096:
-                _tree_workspace_cache.clear()
-            _tree_workspace_cache[key] = need
+        need = _workspace_bytes("tc_paged_tree_attention_workspace", (batch, tokens, q_heads, cache.heads, dim, max_len))
         work = _empty_on(handle, dev, need, _torch.uint8) if need else None
         rc = lib.tc_paged_tree_attention(cache._ref, q.data_ptr(), ql[0], out.data_ptr(), ol[0], code, block_table.data_ptr(), tl[0],
                                          lens, starts, words, max_len, scale, lp, ll[0],

@@ -158,7 +158,7 @@ int64_t paged_logit_row(int64_t max_len);
 // How a call of attention of several rows is dealt out: query rows in tiles of tile_rows, key rows in units of unit_rows, the
 // card filled by parts of tiles (slots, least as in RowsArgs) where tiles are few.
 struct RowsShape {
-  int64_t tile_rows, unit_rows, tiles, slots, least, workgroups;
+  int64_t tile_rows, unit_rows, tiles, slots, least, workgroups, bytes;
 };
 constexpr int64_t kRowsWorkspaceHead = 256;  // bytes: a number, and the parts on lines of their own
 RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);

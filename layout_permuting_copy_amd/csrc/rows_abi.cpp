@@ -70,6 +70,25 @@ void apart_from_inputs(const Operand* const* outs, int n_outs, Operands inputs) 
     for (const Operand* y : inputs) apart("an output and an input", *outs[i], *y);
 }
 
+tc::RowsShape prompt_shape(int64_t batch, int64_t tokens, int64_t keys, int64_t q_heads, int64_t heads, int64_t dim) {
+  return tc::rows_shape(false, false, batch, tokens, heads, q_heads / heads, dim, keys / batch);
+}
+
+// What the call takes of its workspace.
+Operand workspace_of(void* workspace, int64_t workspace_bytes, const tc::RowsShape& shape, int64_t dim, tc::RowsArgs* a) {
+  need(workspace_bytes >= shape.bytes, TC_E_ARG, "workspace too small");
+  need(workspace || shape.bytes == 0, TC_E_NULL, "null workspace");
+  need(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, TC_E_ALIGN, "workspace not aligned to 16 bytes");
+  Operand work{};
+  work.empty = shape.bytes == 0;
+  work.r.lo = reinterpret_cast<uintptr_t>(workspace);
+  work.r.hi = work.r.lo + shape.bytes;
+  a->part_units = static_cast<uint32_t*>(workspace);
+  a->part_o = static_cast<float*>(workspace) + tc::kRowsWorkspaceHead / 4;
+  a->part_ml = a->part_o + shape.workgroups * shape.tile_rows * dim;
+  return work;
+}
+
 void dealt(tc::RowsArgs* a, const tc::RowsShape& shape, int64_t heads, int64_t group) {
   need(shape.workgroups < (int64_t(1) << 31), TC_E_RANGE, "more rows than one launch takes");
   a->heads = int32_t(heads);
@@ -89,7 +108,7 @@ extern "C" {
 int tc_prompt_attention(const void* q, const tc_layout* q_layout, const void* k, const tc_layout* k_layout, const void* v,
                         const tc_layout* v_layout, void* out, const tc_layout* out_layout, int dtype, int64_t batch,
                         const int32_t* token_starts, const int32_t* key_starts, int causal, float scale, float* lse,
-                        const tc_layout* lse_layout, void* stream) {
+                        const tc_layout* lse_layout, void* workspace, int64_t workspace_bytes, void* stream) {
   return guarded([&]() -> int {
     const int eb = float_bytes(dtype);
     tc::RowsArgs a{};
@@ -112,8 +131,10 @@ int tc_prompt_attention(const void* q, const tc_layout* q_layout, const void* k,
       aligned("v", vo, 3);
       need(ko.s[0] < kTokenStride && vo.s[0] < kTokenStride, TC_E_RANGE, "keys or values 2^24 bytes apart from token to token");
     }
-    const Operand* outs[] = {&c.o, &c.l};
-    apart_from_inputs(outs, 2, Operands{&c.q, &ko, &vo, &starts, &kstarts});
+    const tc::RowsShape shape = prompt_shape(batch, tokens, rows, q_heads, heads, dim);
+    const Operand work = workspace_of(workspace, workspace_bytes, shape, dim, &a);
+    const Operand* outs[] = {&c.o, &c.l, &work};
+    apart_from_inputs(outs, 3, Operands{&c.q, &ko, &vo, &starts, &kstarts});
     a.k = ko.p;
     a.v = vo.p;
     a.kt = ko.s[0], a.kh = ko.s[1], a.vt = vo.s[0], a.vh = vo.s[1];
@@ -122,10 +143,20 @@ int tc_prompt_attention(const void* q, const tc_layout* q_layout, const void* k,
     a.key_rows = int32_t(ko.empty ? 0 : rows);
     a.batch = int32_t(batch);
     a.causal = causal;
-    const tc::RowsShape shape = tc::rows_shape(false, false, batch, tokens, heads, q_heads / heads, dim, 0);
     dealt(&a, shape, heads, q_heads / heads);
     return launched(tc::launch_prompt_attention(a, shape, dtype, stream));
   });
+}
+
+int64_t tc_prompt_attention_workspace(int64_t batch, int64_t tokens, int64_t keys, int64_t q_heads, int64_t heads, int64_t head_dim) {
+  int64_t bytes = 0;
+  const int rc = guarded([&]() -> int {
+    rows_sizes(batch, tokens, q_heads, heads, head_dim, 0);
+    need(keys >= 0 && keys <= kMost, TC_E_RANGE, "more than 2^30 keys");
+    if (batch && tokens && q_heads) bytes = prompt_shape(batch, tokens, keys, q_heads, heads, head_dim).bytes;
+    return TC_OK;
+  });
+  return rc == TC_OK ? bytes : rc;
 }
 
 int64_t tc_paged_tree_attention_workspace(int64_t batch, int64_t tokens, int64_t q_heads, int64_t heads, int64_t head_dim,
@@ -165,14 +196,7 @@ int tc_paged_tree_attention(const tc_paged_cache* cache, const void* q, const tc
     }
     if (c.q.empty || batch == 0) return TC_OK;
     const tc::RowsShape shape = tc::rows_shape(true, p.dtype == TC_E4M3, batch, tokens, p.heads, group, p.dim, max_len);
-    const int64_t slots = shape.slots ? shape.workgroups * shape.tile_rows : 0, bytes = slots ? tc::kRowsWorkspaceHead + slots * (p.dim + 2) * 4 : 0;
-    need(workspace_bytes >= bytes, TC_E_ARG, "workspace too small");
-    need(workspace || bytes == 0, TC_E_NULL, "null workspace");
-    need(reinterpret_cast<uintptr_t>(workspace) % 16 == 0, TC_E_ALIGN, "workspace not aligned to 16 bytes");
-    Operand work{};
-    work.empty = bytes == 0;
-    work.r.lo = reinterpret_cast<uintptr_t>(workspace);
-    work.r.hi = work.r.lo + bytes;
+    const Operand work = workspace_of(workspace, workspace_bytes, shape, p.dim, &a);
     const Operand* outs[] = {&c.o, &c.l, &work};
     for (const Operand* x : outs)
       if (touches(p, *x)) refuse(TC_E_ALIAS, "the cache overlaps an output");
@@ -181,9 +205,6 @@ int tc_paged_tree_attention(const tc_paged_cache* cache, const void* q, const tc
     a.lens = reinterpret_cast<const int32_t*>(lens.p);
     a.starts = reinterpret_cast<const int32_t*>(starts.p);
     a.masks = masks ? reinterpret_cast<const int64_t*>(mo.p) : nullptr;
-    a.part_units = static_cast<uint32_t*>(workspace);
-    a.part_o = static_cast<float*>(workspace) + tc::kRowsWorkspaceHead / 4;
-    a.part_ml = a.part_o + slots * p.dim;
     a.batch = int32_t(batch);
     a.causal = 1;
     // no row past the table's columns, and none of an empty pool

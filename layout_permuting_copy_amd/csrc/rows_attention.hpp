@@ -218,7 +218,7 @@ struct RowsWalk {
     const uint32_t upto = wave_scan(sum), total = uint32_t(__builtin_amdgcn_readlane(int(upto), 63));
     const uint32_t before_all = ITEMS ? upto - sum : wave_scan(all) - all;
     if (x >= total) return false;
-    if (REVERSED) x = total - 1 - x;
+    if (REVERSED && !a.slots) x = total - 1 - x;
     // the lanes whose sequences all come before x
     const int l = __popcll(__ballot(upto <= x));
     uint32_t rest = x - uint32_t(__builtin_amdgcn_readlane(int(upto - sum), l));
@@ -329,7 +329,7 @@ void rows_attention_kernel(RowsArgs a) {
 
   RowsWalk<PAGED, BM, KT> walk;
   walk.template init<true>(a);
-  if (PAGED && a.slots && blockIdx.x == 0 && tid == 0) *a.part_units = walk.most;
+  if (a.slots && blockIdx.x == 0 && tid == 0) *a.part_units = walk.most;
   int b;
   uint32_t at, first;
   RowsSeq seq;

@@ -10,9 +10,9 @@ template <bool BF16, int SRC, int DP, int WQ, int WAVES, int PARTS>
 void attend_rows(const RowsArgs& a, hipStream_t s) {
   typedef Rows<BF16, SRC, DP, WQ, WAVES, PARTS> C;
   hipLaunchKernelGGL((rows_attention_kernel<BF16, SRC, DP, WQ, WAVES, PARTS>), dim3(uint32_t(a.workgroups)), dim3(C::THREADS), 0, s, a);
-  if constexpr (C::PAGED)
+  if constexpr (C::PAGED || C::BM <= 128)  // (prompts in tiles of 256 rows are whole)
     if (a.slots)
-      hipLaunchKernelGGL((rows_join_kernel<BF16, true, DP, C::BM, C::KT>), dim3(uint32_t(a.tiles * a.heads * (C::BM / kJoinRows))),
+      hipLaunchKernelGGL((rows_join_kernel<BF16, C::PAGED, DP, C::BM, C::KT>), dim3(uint32_t(a.tiles * a.heads * (C::BM / kJoinRows))),
                          dim3(kRowsThreads), 0, s, a);
 }
 

@@ -9,7 +9,7 @@ namespace {
 
 constexpr int64_t kCus = 256;
 // Workgroups that a compute unit holds: one of eight waves (heads above 128 elements, tiles of 256 rows), else two of four, or three.
-int64_t resident(int64_t head_dim, int64_t tile) { return head_dim > 128 || tile == 256 ? 1 : head_dim > 64 ? 2 : 3; }
+int64_t resident(bool paged, int64_t head_dim, int64_t tile) { return head_dim > 128 || tile == 256 ? 1 : head_dim > 64 || !paged ? 2 : 3; }
 int64_t least_tile(int64_t head_dim) { return head_dim > 128 ? 128 : 64; }
 int64_t tiles_of(int64_t rows, int64_t batch, int64_t tile) { return std::min(rows, rows / tile + batch); }
 
@@ -37,15 +37,22 @@ RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int6
     if (tiles_of(rows, batch, 128) * heads >= 4 * kCus) c.tile_rows = 128;
     if (head_dim > 64 && tiles_of(rows, batch, 256) * heads >= 2 * kCus && rows >= 2048 * batch) c.tile_rows = 256;
   }
+  // Tiles that leave half of the card idle are split over their keys: a cache's always, unless they are short, a prompt's where
+  // its keys (`max_len` is their mean) are long enough for the joining to pay (64 tokens of 32 heads over 8, 8064 keys: 145 us,
+  // split 33; 512 of 8 over 1, 4608 keys: 85 and 35; 1024 causal tokens of 8 over 8: 24 and 27).  Prompts whose tiles come to
+  // more are faster whole (2048 tokens of 16 heads of 256 over 4: 86 us, split 92).
+  bool split = max_len > 512;
+  if (!paged) split = max_len > 1536 && 2 * tiles_of(rows, batch, c.tile_rows) * heads <= kCus * resident(paged, head_dim, c.tile_rows);
   c.unit_rows = 64;
   c.tiles = tiles_of(rows, batch, c.tile_rows);
   c.workgroups = c.tiles * heads;
-  const int64_t fill = kCus * resident(head_dim, c.tile_rows);
-  if (paged && c.workgroups < 2 * fill && max_len > 512) {
+  const int64_t fill = kCus * resident(paged, head_dim, c.tile_rows);
+  if (split && c.workgroups < 2 * fill) {
     c.slots = fill;
     c.least = 2;  // (one tree of 8 tokens over 523 rows: 16.7 us, at least 4 units a part 18.6, one 17.1)
     // all parts fit the least multiple of `fill` that the tiles do
     c.workgroups = (c.workgroups + fill - 1) / fill * fill;
+    c.bytes = kRowsWorkspaceHead + c.workgroups * c.tile_rows * (head_dim + 2) * 4;
   }
   return c;
 }
@@ -54,7 +61,7 @@ int64_t rows_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t gro
   if (max_len <= 512) return 0;
   int64_t most = 0;
   for (int64_t tile = least_tile(head_dim); tile <= 256; tile *= 2) {
-    const int64_t fill = kCus * resident(head_dim, tile);
+    const int64_t fill = kCus * resident(true, head_dim, tile);
     const int64_t workgroups = (std::min(tiles_of(tokens * group, batch, tile) * heads, 2 * fill) + fill - 1) / fill * fill;
     most = std::max(most, kRowsWorkspaceHead + workgroups * tile * (head_dim + 2) * 4);
   }

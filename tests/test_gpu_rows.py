@@ -618,3 +618,21 @@ def test_tree_in_the_largest_tiles(kind, shape):
     _tree(q, pool, table, lens, n, page)
     words = [w for t in n for w in _random_masks(gen, t, "any")]
     _tree(q, pool, table, lens, n, page, words)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads, group, dim, n, m", [
+    (1, 4, 64, [5, 0, 40], [4000, 0, 1200]), (2, 1, 128, [1], [5001]), (2, 8, 128, [17, 20], [1, 4096]), (1, 2, 256, [70, 3, 0], [3001, 2000, 7]),
+    (3, 1, 96, [200], [1700]), (1, 1, 192, [9] * 70, [1600] * 70)])
+def test_prompts_of_few_queries_and_long_keys(kind, causal, heads, group, dim, n, m):
+    """Tiles split over their keys and joined; more sequences than lanes; the same bits again."""
+    gen = torch.Generator().manual_seed(dim + len(n))
+    need = L.load_library().tc_prompt_attention_workspace(len(n), sum(n) + 3, sum(m) + 40, heads * group, heads, dim)
+    assert need > 0
+    say(f"[gpu] {n[:3]} tokens over {m[:3]} keys, {need} bytes")
+    q, k, v = _qkv(gen, P.DT[kind], sum(n) + 3, sum(m) + 40, heads, group, dim)
+    k[sum(m):], v[sum(m):] = math.nan, math.nan
+    out, lse, _ = _prompt(q, k, v, n, m, causal)
+    again, lse_again, _ = _prompt(q, k, v, n, m, causal)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)

@@ -14,11 +14,12 @@ MB = 1 << 20
 
 def _prompt(dtype=L.TC_BF16, q_shape=(30, 4, DIM), k_shape=(30, HEADS, DIM), v_shape=None, out_shape=None, q=BASE, k=BASE + 4 * MB,
             v=BASE + 8 * MB, out=BASE + 12 * MB, q_stride=None, k_stride=None, v_stride=None, out_stride=None, batch=3,
-            starts=BASE + 16 * MB, key_starts=None, causal=1, scale=1.0, lse=None, lse_shape=(30, 4), lse_stride=None, offset=0):
+            starts=BASE + 16 * MB, key_starts=None, causal=1, scale=1.0, lse=None, lse_shape=(30, 4), lse_stride=None, offset=0,
+            work=BASE + 256 * MB, work_bytes=1 << 30):
     ql, kl, vl = _lay(q_shape, q_stride, offset), _lay(k_shape, k_stride), _lay(v_shape or k_shape, v_stride)
     ol, ll = _lay(out_shape or q_shape, out_stride), _lay(lse_shape, lse_stride)
     return L.load_library().tc_prompt_attention(q, _ref(ql), k, _ref(kl), v, _ref(vl), out, _ref(ol), dtype, batch, starts, key_starts,
-                                                causal, scale, lse, _ref(ll), None)
+                                                causal, scale, lse, _ref(ll), work, work_bytes, None)
 
 
 def _tree(cache=None, dtype=L.TC_BF16, q=BASE + 4 * MB, q_shape=(30, 4, DIM), q_stride=None, out=BASE + 8 * MB, out_shape=None,
@@ -84,6 +85,11 @@ PROMPT = [
     (L.TC_E_RANGE, "2^58", lambda: _prompt(q_stride=(BIG, DIM, 1))),
     (L.TC_E_RANGE, "2^30", lambda: _prompt(q_shape=(1 << 29, 4, 16), k_shape=(1 << 29, 2, 16), out_shape=(1 << 29, 4, 16))),
     (L.TC_E_RANGE, "65535", lambda: _prompt(q_shape=(1, 65536, 16), k_shape=(1, 1, 16))),
+    (L.TC_E_ARG, "workspace", lambda: _prompt(k_shape=(6000, HEADS, DIM), key_starts=BASE + 17 * MB, work_bytes=0)),
+    (L.TC_E_NULL, "workspace", lambda: _prompt(k_shape=(6000, HEADS, DIM), key_starts=BASE + 17 * MB, work=None)),
+    (L.TC_E_ALIGN, "workspace", lambda: _prompt(k_shape=(6000, HEADS, DIM), key_starts=BASE + 17 * MB, work=BASE + 256 * MB + 4)),
+    (L.TC_E_ALIAS, "an output", lambda: _prompt(k_shape=(6000, HEADS, DIM), key_starts=BASE + 17 * MB, work=BASE)),
+    (L.TC_E_ALIAS, "two outputs", lambda: _prompt(k_shape=(6000, HEADS, DIM), key_starts=BASE + 17 * MB, work=BASE + 12 * MB)),
     (L.TC_E_RANGE, "keys", lambda: _prompt(q_shape=(1, 1, 16), k_shape=((1 << 30) + 1, 1, 16), key_starts=BASE + 17 * MB)),
 ]
 TREE = [
@@ -223,3 +229,23 @@ def test_the_binding_refuses_on_the_host():
     with pytest.raises(ValueError, match="block_table"):
         L.tc_paged_resize(i(2), i(2), i(2), i(9), i(1), 16)
     assert ctypes.sizeof(L.TcPagedCache) > 0
+
+
+@pytest.mark.parametrize("args, want", [((1, 1, 1, 3, 2, 64), L.TC_E_EXTENT), ((1, 1, -1, 2, 2, 64), L.TC_E_RANGE), ((1, 1, 1, 2, 2, 65), L.TC_E_EXTENT),
+                                        ((-1, 1, 1, 2, 2, 64), L.TC_E_EXTENT), ((0, 5, 5, 2, 2, 64), 0), ((1, 0, 5, 2, 2, 64), 0),
+                                        ((1, 1, 1536, 2, 2, 64), 0), ((1, 1 << 20, 1 << 20, 8, 8, 64), 0)])
+def test_prompt_workspace_sizes(args, want):
+    assert L.load_library().tc_prompt_attention_workspace(*args) == want
+
+
+def test_tree_workspace_suffices_for_smaller_calls():
+    """What is asked at the largest sizes covers every call of fewer sequences, tokens and rows."""
+    import random
+    rng = random.Random(3)
+    size = L.load_library().tc_paged_tree_attention_workspace
+    for _ in range(3000):
+        heads, group, dim = rng.choice([1, 2, 8, 40]), rng.choice([1, 4, 7, 16]), 16 * rng.randint(1, 16)
+        batch, tokens, longest = rng.randint(1, 300), rng.randint(1, 3000), rng.choice([100, 513, 5000, 100000])
+        most = size(batch, tokens, heads * group, heads, dim, longest)
+        for _ in range(4):
+            assert size(rng.randint(1, batch), rng.randint(1, tokens), heads * group, heads, dim, rng.randint(1, longest)) <= most
