@@ -636,3 +636,18 @@ def test_prompts_of_few_queries_and_long_keys(kind, causal, heads, group, dim, n
     out, lse, _ = _prompt(q, k, v, n, m, causal)
     again, lse_again, _ = _prompt(q, k, v, n, m, causal)
     assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
+def test_starts_that_do_not_ascend_stay_inside():
+    """What such a call leaves is its own affair; it ends, keeps to its tensors, and the next one is right."""
+    gen = torch.Generator().manual_seed(21)
+    q, k, v = _qkv(gen, torch.bfloat16, 96, 8000, 1, 4, 64)
+    back = _i32([0, 96, 0, 96, 0, 96, 0, 96, -5, 200])
+    around = torch.full((3, 96, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    L.tc_prompt_attention(q.cuda(), k.cuda(), v.cuda(), back, key_starts=_i32([0, 8000, 0, 8000, 9000, 8000, -3, 8000, 1, 8000]), out=around[1])
+    pool = P.Pool("bf16", 500, 16, 1, 64, "rows", gen)
+    table = torch.arange(500, dtype=torch.int32).reshape(1, 500).expand(9, 500).contiguous()
+    L.tc_paged_tree_attention(q.cuda(), pool.on_gpu(), table.cuda(), _i32([8000] * 9), back, out=around[1])
+    assert bool((around[0] == 7.0).all()) and bool((around[2] == 7.0).all())
+    _prompt(q, k, v, [96], [8000])
+    _tree(q, pool, table[:1], [8000], [96], 16)
