@@ -752,6 +752,7 @@ void rows_attention_kernel(RowsArgs a) {
               y -= high_half<VBF>(w);
             }
           }
+          if constexpr (DP > 192 && PARTS > 1) __builtin_amdgcn_sched_barrier(0);
         }
 
       if constexpr (DP > 192) __builtin_amdgcn_sched_barrier(0);  // (one product's registers at a time)

@@ -6,13 +6,17 @@
 namespace tc {
 namespace dev {
 
+// 8-bit rows' weights are bf16 values, as their scales may pass fp16's range: for fp16 queries the sum of two in every tile (one
+// holds 8 bits, fewer than out; 16 trees of 12 tokens over 8192 rows 153 us, with one 133), else in tiles of 64 rows, whose
+// matrix units wait for memory anyway.
 template <bool BF16, int SRC, int DP, int PARTS>
 void tree_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
+  constexpr int LARGE = SRC == 2 && !BF16 ? 2 : 1;
   if constexpr (DP > 64 && !(SRC == 2 && DP > 128))
-    if (shape.tile_rows == 256) return attend_rows<BF16, SRC, DP, 8, 8, 1>(a, s);
-  if constexpr (DP > 128) return attend_rows<BF16, SRC, DP, 4, 8, 1>(a, s);
+    if (shape.tile_rows == 256) return attend_rows<BF16, SRC, DP, 8, 8, LARGE>(a, s);
+  if constexpr (DP > 128) return attend_rows<BF16, SRC, DP, 4, 8, LARGE>(a, s);
   else if (shape.tile_rows == 64) return attend_rows<BF16, SRC, DP, 2, 4, PARTS>(a, s);
-  else return attend_rows<BF16, SRC, DP, 4, 4, 1>(a, s);
+  else return attend_rows<BF16, SRC, DP, 4, 4, LARGE>(a, s);
 }
 
 template <bool BF16, int SRC>

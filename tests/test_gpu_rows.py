@@ -651,3 +651,16 @@ def test_starts_that_do_not_ascend_stay_inside():
     assert bool((around[0] == 7.0).all()) and bool((around[2] == 7.0).all())
     _prompt(q, k, v, [96], [8000])
     _tree(q, pool, table[:1], [8000], [96], 16)
+
+
+@pytest.mark.parametrize("shape", LARGE + TREES[:5], ids=lambda s: "x".join(map(str, s[:4])))
+def test_fp16_over_8_bit_rows_keeps_its_bits(shape):
+    """Weights there are the sum of two bf16 values, off by the square of half a bf16 step (2^-8), in tiles of every size."""
+    heads, group, dim, page, major, lens, n = shape
+    gen = torch.Generator().manual_seed(dim + page)
+    table, pages = P.table_for(lens, page, gen, spare=1)
+    pool = P.Pool("e4m3", pages, page, heads, dim, major, gen)
+    q = torch.randn(sum(n), heads * group, dim, generator=gen).to(torch.float16)
+    out, _, _ = _tree(q, pool, table, lens, n, page)
+    ref = _tree_ref(q, pool, table, lens, n, page, None, part=2.0 ** -16)
+    R.close(out, ref[0], ref[2], "out", torch.float16)
