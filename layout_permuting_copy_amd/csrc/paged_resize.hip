@@ -73,13 +73,15 @@ __device__ __forceinline__ void place(const ResizeArgs& a, int b, int row, int64
 
 // One workgroup: sequences 1024 at a time, a lane each, their pages and tokens numbered by running sums; then a lane a page or
 // token, its sequence found among the sums in LDS.  Pages that come back go onto the stack first, as far as they are pages and
-// it has room; then those needed come off it.  PLACES: the new rows' places too.  Bound: its launch and a few dependent trips
-// to memory, which is why one workgroup does it all.
+// it has room; then those needed come off it.  PLACES: the new rows' places too; else only those of the one sequence whose
+// rows the starts no longer count, as they stop at kMostRows (paged_places_kernel finds a row from where its sequence ends).
+// Bound: its launch and a few dependent trips to memory, which is why one workgroup does it all.
 template <bool PLACES>
 __global__ __launch_bounds__(kResizeThreads) void paged_resize_kernel(ResizeArgs a) {
   __shared__ uint32_t shared[kResizeWaves];
   __shared__ uint32_t sums[kResizeThreads], token_sums[PLACES ? kResizeThreads : 1];
   __shared__ int from[kResizeThreads], row_from[PLACES ? kResizeThreads : 1];
+  __shared__ int past, past_row;  // the sequence that passes kMostRows, its first new row
   const int tid = threadIdx.x, batch = a.table.batch, cols = a.table.cols;
   const auto length = [&](int b) { return a.lens[b] > 0 ? a.lens[b] : 0; };
   const int held = a.free_count[0];
@@ -117,12 +119,14 @@ __global__ __launch_bounds__(kResizeThreads) void paged_resize_kernel(ResizeArgs
   for (int b0 = 0; b0 < batch; b0 += kResizeThreads) {
     const int b = b0 + tid, count = batch - b0 < kResizeThreads ? batch - b0 : kResizeThreads;
     uint32_t take = 0, grow = 0;
+    int from_row = 0;
     if (b < batch) {
       const int n = length(b), now = resized(n, a.change[b]);
       const int first = columns_of(n, a.page, cols), last = columns_of(now, a.page, cols);
       take = last > first ? uint32_t(last - first) : 0u;
       grow = now > n ? uint32_t(now - n) : 0u;
       from[tid] = first;
+      from_row = n;
       if (PLACES) row_from[tid] = n;
       a.lens_out[b] = now;
     }
@@ -131,7 +135,9 @@ __global__ __launch_bounds__(kResizeThreads) void paged_resize_kernel(ResizeArgs
     if (a.starts) {
       const uint32_t before = sums_before(grow, shared, &all);
       if (PLACES) token_sums[tid] = before;
-      if (b < batch) a.starts[b] = int32_t(sum_to_most(tokens, before));
+      const uint32_t start = sum_to_most(tokens, before);
+      if (b < batch) a.starts[b] = int32_t(start);
+      if (!PLACES && grow && start < uint32_t(kMostRows) && sum_to_most(start, grow) == uint32_t(kMostRows)) past = b, past_row = from_row;
     }
     __syncthreads();
     for (uint32_t t = tid; t < total; t += kResizeThreads) {
@@ -148,6 +154,10 @@ __global__ __launch_bounds__(kResizeThreads) void paged_resize_kernel(ResizeArgs
         const int i = find_start(token_sums, count, t);
         place(a, b0 + i, row_from[i] + int(t - token_sums[i]), to);
       }
+    } else if (tokens < uint32_t(kMostRows) && sum_to_most(tokens, all) == uint32_t(kMostRows)) {
+      __syncthreads();
+      const int start = a.starts[past];
+      for (int64_t t = int64_t(start) + tid; t < a.tokens; t += kResizeThreads) place(a, past, past_row + int(t - start), t);
     }
     tokens = sum_to_most(tokens, all);
     __syncthreads();
@@ -164,7 +174,9 @@ __global__ __launch_bounds__(kResizeThreads) void paged_resize_kernel(ResizeArgs
     }
 }
 
-// The places of many new rows, four a lane, once the pages are in the table.
+// The places of many new rows, four a lane, once the pages are in the table.  A row counts back from its sequence's end, since
+// lens_out may have taken the place of the old lengths; where that end is kMostRows the sums stopped, and the first kernel
+// has placed the rows.
 __global__ __launch_bounds__(kPlaceThreads) void paged_places_kernel(ResizeArgs a) {
   __shared__ uint32_t held[kPlaceStarts];
   const int batch = a.table.batch;
@@ -196,6 +208,7 @@ __global__ __launch_bounds__(kPlaceThreads) void paged_places_kernel(ResizeArgs 
       while (t >= end);
       row = a.lens_out[b] - (end - int(t));
     }
+    if (end == kMostRows) return;
     place(a, b, row, t);
   }
 }

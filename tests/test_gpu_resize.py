@@ -120,6 +120,26 @@ def test_resize_at_the_edges():
     assert n.tolist() == [8, 2] and slots.tolist() == [-1] * 3 and count.tolist() == [3]
 
 
+@pytest.mark.parametrize("tokens", [64, 8192, 8193, 20000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rows_of_the_sequence_past_which_the_starts_stop(tokens, in_place):
+    """A sequence whose end the starts no longer count has its rows counted from its own first, also where its old length
+    cannot be had from its new one."""
+    most = 2 ** 31 - 1
+    for lens, change in (([0, 0], [5000, most]), ([0, 7], [10, most]), ([33, 100, 4], [-33, most - 99, 9]), ([5, 0, 40, 3], [0, 17, most, most]),
+                         ([2], [most - 2]), ([2], [most]), ([0] * 1500 + [21, 6], [3] * 1500 + [most - 5000, 9]),
+                         ([most - 3, 0], [3, most - 3]), ([9] * 1025, [0] * 1024 + [most])):
+        held = [min(-(-n // 16), 700) for n in lens]
+        order = list(range(sum(held) + 900))
+        random.Random(len(lens)).shuffle(order)
+        table, at = [], 0
+        for h in held:
+            table.append(order[at:at + h] + [-1] * (700 - h))
+            at += h
+        say(f"[gpu] {lens[:4]} + {change[:4]}, {tokens} places")
+        _check(table, lens, change, order[at:] + [-1] * at, 900, 16, tokens, in_place=in_place)
+
+
 def test_resize_of_a_strided_table_without_the_rows_places():
     rng = random.Random(5)
     table, lens, change, stack, free = _case(rng, 40, 16, 200, "mixed")
