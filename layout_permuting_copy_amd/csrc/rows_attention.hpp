@@ -46,9 +46,11 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // 16 bytes a lane from memory straight into LDS, at `lds` + 16 * lane, of the lanes that are on.  Nothing waits for them but
-// loads_landed() (the compiler knows of no register that they write, and what it waits for on its own account is older).
+// loads_landed() (the compiler knows of no register that they write, and what it waits for on its own account is older).  Of a
+// range: its scalar registers and offset may come from a vector instruction (read-lane) right before, and the compiler does not look
+// inside: a load reads them five wait states later at least, which the move and the pause after it are.
 __device__ __forceinline__ void to_lds(const u32x4& rsrc, uint32_t offset, uint32_t more, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(offset), "s"(rsrc),
                   "s"(__builtin_amdgcn_readfirstlane(int(more))) : "memory");
 }
