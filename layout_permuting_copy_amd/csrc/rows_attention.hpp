@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 __device__ __forceinline__ void to_lds(const u32x4& rsrc, uint32_t offset, uint32_t more, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(offset), "s"(rsrc),
-                  "s"(__builtin_amdgcn_readfirstlane(int(more))) : "memory");
+                  "s"(__builtin_amdgcn_readfirstlane(int(more))) : "memory", "m0");
 }
 __device__ __forceinline__ u32x4 range_of(const unsigned char* base, uint32_t bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
@@ -60,11 +60,11 @@ __device__ __forceinline__ u32x4 range_of(const unsigned char* base, uint32_t by
                uint32_t(__builtin_amdgcn_readfirstlane(int(bytes))), uint32_t(kRsrcWord3)};
 }
 __device__ __forceinline__ void to_lds(const unsigned char* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(p) : "memory", "m0");
 }
 // (4 bytes a lane)
 __device__ __forceinline__ void to_lds(const float* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(p) : "memory", "m0");
 }
 __device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 

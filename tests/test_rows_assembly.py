@@ -67,3 +67,17 @@ def test_loads_wait_for_scalars_from_vector_instructions(listings):
                 j -= 1
     assert loads > 500
     assert not early, (len(early), early[:3])
+
+
+def test_assembly_names_the_registers_that_it_writes():
+    """Scalar registers that a statement's instructions write by name are among its clobbers, m0 and the condition code too."""
+    with open(os.path.join(B.CSRC, "rows_attention.hpp")) as f:
+        text = f.read()
+    written = 0
+    for statement in re.findall(r"\basm(?: volatile)?\s*\(.*?\)\s*;", text, re.S):
+        clobbers = statement.rsplit(":", 1)[1]
+        for pattern, name in ((r"s_mov_b32 m0", "m0"), (r"s_cmp_", "scc")):
+            if re.search(pattern, statement):
+                written += 1
+                assert f'"{name}"' in clobbers, statement[:120]
+    assert written >= 4
