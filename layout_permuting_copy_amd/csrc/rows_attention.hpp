@@ -49,6 +49,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // loads_landed() (the compiler knows of no register that they write, and what it waits for on its own account is older).  Of a
 // range: its scalar registers and offset may come from a vector instruction (read-lane) right before, and the compiler does not look
 // inside: a load reads them five wait states later at least, which the move and the pause after it are.
+// m0 is named because the compiler sets it too, for itself, and merges equal settings; that it is reserved is what it warns of.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void to_lds(const u32x4& rsrc, uint32_t offset, uint32_t more, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(offset), "s"(rsrc),
@@ -66,6 +69,7 @@ __device__ __forceinline__ void to_lds(const unsigned char* p, uint32_t lds) {
 __device__ __forceinline__ void to_lds(const float* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(__builtin_amdgcn_readfirstlane(int(lds))), "v"(p) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
