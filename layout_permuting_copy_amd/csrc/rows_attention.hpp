@@ -14,9 +14,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kRowsThreads = 256;
-// The exponents' reference follows a row's maximum only where that has grown by more than this (base 2): weights stay below
-// 2^8 and sums below 2^8 times their count, far inside fp32's range, and the output is rescaled in few tiles.
-constexpr float kSlack = 8.0f;
+// The exponents' reference follows a row's maximum only where that has grown by more than this (base 2), so the output is
+// rescaled in few tiles.  Weights of bf16 values are held at 2^-8 of what they are, at most 1 then: sums of weights times values
+// pass fp32's range where those of exp(x - max x) |v| do, and no earlier (bf16 holds such weights as exactly).
+constexpr int kSlackBits = 8;
+constexpr float kSlack = kSlackBits;
 
 // D = A B + C on 32 x 32 tiles with a contraction of 16.  Lane l (r = l % 32, h = l / 32) holds row r of A and column r of
 // B at contraction indices 8 h .. 8 h + 7, and of C and D column r at rows 8 (i / 4) + 4 h + i % 4, i = 0 .. 15.
@@ -99,6 +101,13 @@ __device__ __forceinline__ void scale_if(f32x16& x, float f, uint32_t need) {
         : "v"(f), "s"(need)
         : "scc");
   x = f32x16{x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, x10, x11, x12, x13, x14, x15};
+}
+
+// 2^-RAISE
+template <int RAISE>
+constexpr float unraise() {
+  if constexpr (RAISE < 0) return float(1 << -RAISE);
+  else return 1.0f / float(1 << RAISE);
 }
 
 // The log of a row's sum, by its maximum (of q k, before the scale) and its sum relative to that.
@@ -289,7 +298,8 @@ struct Rows {
   static constexpr int RPW = 64 / CPR;            // rows a wave loads at once
   static constexpr int RPP = WAVES * RPW;             // and a workgroup
   static constexpr int PASSES = KT / RPP;
-  static constexpr int RAISE = VBF ? 0 : 7;
+  // weights are held 2^RAISE as large: fp16 ones above where its numbers grow coarse
+  static constexpr int RAISE = VBF ? -kSlackBits : 7;
   static constexpr int TILE_BYTES = KT * PB, PASS_BYTES = 1024 * WAVES;
   static_assert(NSUB >= 1 && RPP % 16 == 0, "a wave has 32 key rows at least, a pass rows of the same exchange");
   // where the groups of waves meet: all but the first leave their outputs in LDS
@@ -719,10 +729,12 @@ void rows_attention_kernel(RowsArgs a) {
         ref = 0.0f;
       }
       ref = finite(ref);
+      if constexpr (C::RAISE < 0) ref -= C::RAISE;  // (a reference like another: sums of weights are relative to it as well)
       constexpr int CHAINS = DP > 128 ? 1 : 4;  // of additions
       float sum[CHAINS] = {l};
       const auto weight = [&](int n, int i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, -ref)) * float(1 << C::RAISE);
+        float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, -ref));
+        if constexpr (C::RAISE > 0) e *= float(1 << C::RAISE);
         sum[i % CHAINS] += e;
         return e;
       };
@@ -833,7 +845,7 @@ void rows_attention_kernel(RowsArgs a) {
   const bool real = row < rows;
   if (parts > 1) {
     const int64_t slot = int64_t(blockIdx.x) * BM + local;
-    if (end_hl == 0) a.part_ml[2 * slot] = m, a.part_ml[2 * slot + 1] = l * (1.0f / float(1 << C::RAISE));
+    if (end_hl == 0) a.part_ml[2 * slot] = m, a.part_ml[2 * slot + 1] = l;
 #pragma unroll
     for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -841,7 +853,7 @@ void rows_attention_kernel(RowsArgs a) {
         const int d = 32 * f + 8 * i + 4 * end_hl;
         f32x4 y;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = o[f][4 * i + j] * (1.0f / float(1 << C::RAISE));
+        for (int j = 0; j < 4; ++j) y[j] = o[f][4 * i + j];
         if (real && d < a.head_dim) *reinterpret_cast<f32x4*>(a.part_o + slot * a.head_dim + d) = y;
       }
     return;
@@ -865,7 +877,7 @@ void rows_attention_kernel(RowsArgs a) {
       if (real && d < a.head_dim) *reinterpret_cast<u32x4*>(out + 2 * d) = u32x4{e0[0], e1[0], e0[1], e1[1]};
     }
   if (a.lse && real && end_hl == 0)
-    a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] = lse_of(m, l * (1.0f / float(1 << C::RAISE)), a.scale);
+    a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] = lse_of(m, l * unraise<C::RAISE>(), a.scale);
 }
 
 // The parts of a tile's query rows joined, a few lanes a row (32, or 64 above 128 elements): the parts' maxima give their
@@ -873,7 +885,7 @@ void rows_attention_kernel(RowsArgs a) {
 // end at once.  Bound: its launch and three trips to memory one after another (lengths; the parts' sums and first outputs
 // together; the rest); 34 MB of parts of 32 trees 9.7 us, 14.3 where every row's sums were waited for before its outputs.
 constexpr int kJoinRows = 16;
-template <bool BF16, bool PAGED, int DP, int BM, int KT>
+template <bool BF16, bool PAGED, int DP, int BM, int KT, int RAISE>
 __global__ __launch_bounds__(kRowsThreads) void rows_join_kernel(RowsArgs a) {
   constexpr int LPR = DP <= 128 ? 32 : 64, AT_ONCE = kRowsThreads / LPR, CHUNKS = BM / kJoinRows, MINE = kJoinRows / AT_ONCE;
   const int lane = threadIdx.x % LPR;
@@ -962,7 +974,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_join_kernel(RowsArgs a) {
       *reinterpret_cast<u32x2*>(out + 8 * lane) = u32x2{pack2<BF16>(all[z][0] * inv, all[z][1] * inv), pack2<BF16>(all[z][2] * inv, all[z][3] * inv)};
     }
     if (a.lse && lane == 0)
-      a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] = lse_of(top[z], total[z], a.scale);
+      a.lse[int64_t(seq.t0 + tok) * a.lt + (int64_t(h) * a.group + g) * a.lh] = lse_of(top[z], total[z] * unraise<RAISE>(), a.scale);
   }
 }
 

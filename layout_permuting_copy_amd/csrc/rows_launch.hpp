@@ -12,7 +12,7 @@ void attend_rows(const RowsArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((rows_attention_kernel<BF16, SRC, DP, WQ, WAVES, PARTS>), dim3(uint32_t(a.workgroups)), dim3(C::THREADS), 0, s, a);
   if constexpr (C::PAGED || C::BM <= 128)  // (prompts in tiles of 256 rows are whole)
     if (a.slots)
-      hipLaunchKernelGGL((rows_join_kernel<BF16, C::PAGED, DP, C::BM, C::KT>), dim3(uint32_t(a.tiles * a.heads * (C::BM / kJoinRows))),
+      hipLaunchKernelGGL((rows_join_kernel<BF16, C::PAGED, DP, C::BM, C::KT, C::RAISE>), dim3(uint32_t(a.tiles * a.heads * (C::BM / kJoinRows))),
                          dim3(kRowsThreads), 0, s, a);
 }
 
