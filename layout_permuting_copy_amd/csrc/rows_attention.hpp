@@ -103,6 +103,10 @@ __device__ __forceinline__ void scale_if(f32x16& x, float f, uint32_t need) {
   x = f32x16{x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, x10, x11, x12, x13, x14, x15};
 }
 
+// Where a reference m c is this large or more, logits take the difference x - m before they take the factor: x c - (m c) leaves what
+// rounding took of m c, half a step of it (2^-10 from here on; at 2^34 weights pass fp32's range, and m c itself may where m does not).
+constexpr float kFar = 16384.0f;
+
 // 2^-RAISE
 template <int RAISE>
 constexpr float unraise() {
@@ -721,9 +725,9 @@ void rows_attention_kernel(RowsArgs a) {
 #pragma unroll
         for (int f = 0; f < NF; ++f) o[f] *= shrink;
       }
-      // x log2 e may pass fp32's range where x does not (keys of the type's lowest value): then the difference comes first
+      // far from zero (keys of the type's lowest value) the difference comes first
       float ref = m * c;
-      if (any_lane(__builtin_fabsf(ref) == kInf && __builtin_fabsf(m) < kInf)) {
+      if (any_lane(__builtin_fabsf(ref) >= kFar && __builtin_fabsf(m) < kInf)) {
 #pragma unroll
         for (int n = 0; n < NJ; ++n) s[n] -= finite(m);
         ref = 0.0f;

@@ -1,4 +1,4 @@
-"""Attention of several query rows at the ends of its ranges: values near the end of fp32's."""
+"""Attention of several query rows at the ends of its ranges: values near the end of fp32's, logits far from zero."""
 
 import pytest
 import torch
@@ -62,3 +62,71 @@ def test_tree_values_near_the_end_of_the_range(kind, dim, tokens, rows):
     for words in (None, _random_masks(gen, tokens, "tree")):
         out, _, ref = _tree(q, pool, table, [rows], [tokens], 16, words, scale=1.0, max_len=rows)
         assert bool(out.isfinite().all()) and float(ref[0].abs().max()) > 1e36 / rows
+
+
+def _far(kind, x, rows, tokens, dim, gen):
+    """Keys whose logits (scale 1) are exactly x where queries see them, and the definition with x taken off all of them, whose
+    weights are the same: bounds without the logits' own rounding, of which there is none."""
+    dt = torch.bfloat16 if kind == "e4m3" else P.DT[kind]
+    most = 1.0 if kind == "e4m3" else 2.0 ** 14 if kind == "fp16" else 1.0
+    q, k = torch.zeros(tokens, 2, dim, dtype=torch.float32), torch.zeros(rows, 1, dim)
+    q[:, :, 0], k[:, :, 0] = most, (x / most)[:, None]
+    assert bool((q.to(dt).double()[:1, 0, 0] * k.to(dt).double()[:, 0, 0] == x.double()).all())
+    v = torch.randn(rows, 1, dim, generator=gen).to(dt)
+    return q.to(dt), k.to(dt), v
+
+
+FAR = [(kind, x) for kind in ("bf16", "fp16") for x in (2.0 ** 24, 3 * 2.0 ** 26, 5 * 2.0 ** 25, -5 * 2.0 ** 25, -1.75 * 2.0 ** 28, 2.0 ** 28, -7 * 2.0 ** 26)]
+FAR += [("bf16", x) for x in (-1.5 * 2.0 ** 33, 2.0 ** 40, -1.25 * 2.0 ** 63, 1.25 * 2.0 ** 63, -2.0 ** 100, 1.75 * 2.0 ** 99, -1.25 * 2.0 ** 126, 2.0 ** 127)]
+
+
+@pytest.mark.parametrize("kind, x", FAR)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_logits_far_from_zero(kind, x, dim):
+    """Equal logits share the weight, a greater one has it all, wherever they lie; a rise to x comes in the middle."""
+    gen = torch.Generator().manual_seed(3)
+    n = 200
+    levels = torch.full((n,), x)
+    for name, xs in (("equal", levels), ("rise", torch.where(torch.arange(n) < 100, 0.5 * levels if x > 0 else 2 * levels, levels)),
+                     ("few", torch.where(torch.arange(n) % 67 == 5, levels, 0.5 * levels if x > 0 else 2 * levels))):
+        if not bool(xs.isfinite().all()):
+            continue
+        q, k, v = _far(kind, xs, n, n, dim, gen)
+        seen = R.before(n, n)
+        top = torch.where(seen, xs[None, :], -torch.inf).amax(1)
+        flat = torch.zeros_like(k)
+        ref = R.sequence(q, flat, v, seen & (xs[None, :] == top[:, None]))  # the others' weights are 0 in any precision
+        out, lse = torch.zeros_like(q, device="cuda"), torch.zeros(n, 2, device="cuda")
+        say(f"[gpu] {name} {x}")
+        L.tc_prompt_attention(q.cuda(), k.cuda(), v.cuda(), torch.tensor([0, n], dtype=torch.int32, device="cuda"), scale=1.0, out=out, lse=lse)
+        R.close(out, ref[0], ref[2], "out", q.dtype)
+        want = ref[1] + top[:, None].double()
+        R.close(lse, want, ref[3] + 4 * R.STEP32 * want.abs(), "lse")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("x", [5 * 2.0 ** 25, -5 * 2.0 ** 25, -7 * 2.0 ** 26])
+@pytest.mark.parametrize("rows", [90, 2500])
+def test_tree_logits_far_from_zero(kind, x, rows):
+    """Equal logits over a cache, whole and in parts; 8-bit rows by their scales."""
+    gen = torch.Generator().manual_seed(4)
+    tokens, dim = 6, 64
+    table, pages = P.table_for([rows], 16, gen)
+    pool = P.Pool(kind, pages, 16, 1, dim, "rows", gen)
+    q, k, v = _far(kind, torch.full((rows,), x), rows, tokens, dim, gen)
+    at, row = table[0][torch.arange(rows) // 16].long(), torch.arange(rows) % 16
+    if kind == "e4m3":
+        P.bits(pool.k)[at, row] = P.bits(torch.zeros_like(k, dtype=torch.float32).to(torch.float8_e4m3fn))
+        P.bits(pool.k)[at, row, :, 0] = P.bits(torch.ones(1).to(torch.float8_e4m3fn))[0]
+        pool.ks[at, row] = x
+        v = pool.rows("v", table[0], rows, 16)[0]
+    else:
+        pool.k[at, row], pool.v[at, row] = k, v
+    seen = R.before(tokens, rows)
+    part = None if kind != "e4m3" else R.half_step(torch.bfloat16)
+    ref = R.sequence(q, torch.zeros_like(k), v, seen, part=part)
+    lse = torch.zeros(tokens, 2, device="cuda")
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")
+    out = L.tc_paged_tree_attention(q.cuda(), pool.on_gpu(), table.cuda(), i32([rows]), i32([0, tokens]), scale=1.0, lse=lse, max_len=rows)
+    R.close(out, ref[0], ref[2], "out", q.dtype)
+    R.close(lse, ref[1] + x, ref[3] + 4 * R.STEP32 * abs(x), "lse")
