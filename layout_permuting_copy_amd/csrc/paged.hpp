@@ -160,6 +160,8 @@ int64_t paged_logit_row(int64_t max_len);
 struct RowsShape {
   int64_t tile_rows, unit_rows, tiles, slots, least, workgroups, bytes;
 };
+// Lanes of a workgroup: eight waves for wide heads and the largest tiles, else four.
+constexpr int64_t rows_threads(int64_t head_dim, int64_t tile_rows) { return head_dim > 128 || tile_rows == 256 ? 512 : 256; }
 constexpr int64_t kRowsWorkspaceHead = 256;  // bytes: a number, and the parts on lines of their own
 RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 // Bytes that suffice for the parts of tiles at these sizes and at any smaller batch, tokens and max_len.

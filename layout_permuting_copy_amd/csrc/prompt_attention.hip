@@ -26,7 +26,7 @@ void prompt_by_dim(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
 
 int launch_prompt_attention(const RowsArgs& a, const RowsShape& shape, int dtype, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (!launchable(a.workgroups, dev::kRowsThreads)) return TC_E_RANGE;
+  if (!launchable(a.workgroups, rows_threads(a.head_dim, shape.tile_rows))) return TC_E_RANGE;
   if (dtype == TC_BF16)
     dev::prompt_by_dim<true>(a, shape, s);
   else
