@@ -162,6 +162,12 @@ struct RowsShape {
 };
 // Lanes of a workgroup: eight waves for wide heads and the largest tiles, else four.
 constexpr int64_t rows_threads(int64_t head_dim, int64_t tile_rows) { return head_dim > 128 || tile_rows == 256 ? 512 : 256; }
+// Up to so many sequences a workgroup adds up the tiles before its own, each wave all of them; whole tiles of more are numbered so
+// that few steps find one, with a number for nobody a sequence where tiles are full.  (Prompts of 32 tokens, 4 heads a group, 8
+// key heads: 512 of them added up 123 us, numbered 151; 768 206 and 224; 2048 1248 and 590.  Trees of 16 tokens, 8 heads a
+// group, 1 key head, over 256 rows: 512 32 and 43; 1536 119 and 121; 2048 216 and 159.  Prompts of one token, 8 heads: 32768 142
+// ms and 3.)
+constexpr int64_t kRowsSummed = 1536;
 constexpr int64_t kRowsWorkspaceHead = 256;  // bytes: a number, and the parts on lines of their own
 RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 // Bytes that suffice for the parts of tiles at these sizes and at any smaller batch, tokens and max_len.

@@ -222,10 +222,33 @@ struct RowsWalk {
     }
     most = hi;
   }
+  // Whole tiles of many sequences (kRowsSummed): those of sequence b are numbered from (its first row over all sequences) / BM
+  // + b on.  Up to the next sequence's that leaves room for all of them, at most one number more, and the numbers ascend with
+  // b: the 64 lanes look for x's sequence in log64 of their count steps.
+  static __device__ __forceinline__ uint32_t place(const RowsArgs& a, int b) {
+    return uint32_t(within(a.starts[b], 0, a.tokens) * a.group) / BM + uint32_t(b);
+  }
+  __device__ __forceinline__ bool find_among_many(const RowsArgs& a, uint32_t x, int* b, uint32_t* at, RowsSeq* s) const {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, span = a.batch;
+    while (span > 1) {
+      const int step = (span + 63) / 64, probe = lane * step;
+      const int k = __popcll(__ballot(probe < span && place(a, lo + probe) <= x)), skip = k > 1 ? (k - 1) * step : 0;
+      lo += skip;
+      span = step < span - skip ? step : span - skip;
+    }
+    const RowsSeq q = rows_seq<PAGED>(a, lo);
+    s->t0 = __builtin_amdgcn_readfirstlane(q.t0), s->n = __builtin_amdgcn_readfirstlane(q.n);
+    s->k0 = __builtin_amdgcn_readfirstlane(q.k0), s->m = __builtin_amdgcn_readfirstlane(q.m);
+    *b = lo;
+    *at = x - uint32_t(__builtin_amdgcn_readfirstlane(int(place(a, lo))));
+    return *at < tiles(a, *s);
+  }
   // Finds sequence and place of item x (REVERSED: counted from the last; ITEMS: parts of tiles, else tiles); `first`: the
   // number of the sequence's first item of parts.
   template <bool REVERSED, bool ITEMS>
   __device__ __forceinline__ bool find(const RowsArgs& a, uint32_t x, int* b, uint32_t* at, uint32_t* first, RowsSeq* s) const {
+    if (a.batch > kRowsSummed && !a.slots) return find_among_many(a, REVERSED ? uint32_t(a.tiles) - 1 - x : x, b, at, s);
     const int lane = threadIdx.x & 63;
     uint32_t sum = 0, all = 0;
     for (int k = 0; k < per && lane * per + k < a.batch; ++k) {

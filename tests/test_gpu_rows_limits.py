@@ -1,4 +1,8 @@
-"""Attention of several query rows at the ends of its ranges: values near the end of fp32's, logits far from zero."""
+"""Attention of several query rows at the ends of its ranges: values near the end of fp32's, logits far from zero, many
+sequences."""
+
+import random
+import time
 
 import pytest
 import torch
@@ -7,7 +11,7 @@ import layout_permuting_copy_amd as L
 import paged_ref as P
 import rows_ref as R
 from gpu_util import say
-from test_gpu_rows import _prompt, _random_masks, _tree
+from test_gpu_rows import _prompt, _prompt_ref, _random_masks, _tree
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +134,80 @@ def test_tree_logits_far_from_zero(kind, x, rows):
     out = L.tc_paged_tree_attention(q.cuda(), pool.on_gpu(), table.cuda(), i32([rows]), i32([0, tokens]), scale=1.0, lse=lse, max_len=rows)
     R.close(out, ref[0], ref[2], "out", q.dtype)
     R.close(lse, ref[1] + x, ref[3] + 4 * R.STEP32 * abs(x), "lse")
+
+
+def _counts(pattern, batch):
+    """Tokens of each sequence: some of none, some of more than a tile."""
+    rng = random.Random(f"{pattern} {batch}")
+    few = {"ones": lambda i: 1, "sparse": lambda i: 3 if i % 41 == 7 else 0, "ragged": lambda i: rng.choice([0, 0, 1, 2, 5, 13]),
+           "one long": lambda i: 300 if i == batch // 2 else i % 2, "last": lambda i: 70 * (i == batch - 1), "first": lambda i: 70 * (i == 0),
+           "none": lambda i: 0}
+    return [few[pattern](i) for i in range(batch)]
+
+
+MANY = [(p, b) for p in ("ones", "sparse", "ragged", "one long", "last", "first", "none") for b in (65, 1537)] + [("ragged", 1536), ("sparse", 5000)]
+
+
+@pytest.mark.parametrize("pattern, batch", MANY)
+@pytest.mark.parametrize("heads, group, dim, lead", [(2, 5, 64, 75), (1, 1, 256, 0)])
+def test_prompts_of_many_sequences(pattern, batch, heads, group, dim, lead):
+    """Tokens before the first sequence and behind the last belong to none, and stay as they are."""
+    gen = torch.Generator().manual_seed(batch)
+    n = _counts(pattern, batch)
+    total, tokens = sum(n), lead + sum(n) + 9
+    dt = torch.bfloat16 if batch % 2 else torch.float16
+    q, k, v = (torch.randn(tokens, h, dim, generator=gen).to(dt) for h in (heads * group, heads, heads))
+    starts = torch.tensor([lead + x for x in R.starts_of(n)], dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0, device="cuda"), torch.full((tokens, heads * group), 7.0, device="cuda")
+    say(f"[gpu] {batch} sequences, {total} tokens")
+    L.tc_prompt_attention(q.cuda(), k.cuda(), v.cuda(), starts, out=out, lse=lse)
+    if total:
+        at = slice(lead, lead + total)
+        ref = _prompt_ref(q[at], k[at], v[at], n, n, True)
+        R.close(out[at], ref[0], ref[2], "out", dt)
+        R.close(lse[at], ref[1], ref[3], "lse")
+    rest = torch.ones(tokens, dtype=torch.bool)
+    rest[lead:lead + total] = False
+    assert bool((out[rest.cuda()] == 7.0).all()) and bool((lse[rest.cuda()] == 7.0).all())
+
+
+@pytest.mark.parametrize("pattern, batch", [(p, b) for p, b in MANY if b < 2000])
+@pytest.mark.parametrize("heads, group, dim", [(1, 4, 64), (1, 1, 192)])
+def test_trees_of_many_sequences(pattern, batch, heads, group, dim):
+    gen = torch.Generator().manual_seed(batch)
+    n = _counts(pattern, batch)
+    lens = [max(x, (37 * i) % 50 + (x > 0) * (i % 3 == 0) * 90) for i, x in enumerate(n)]
+    table, pages = P.table_for(lens, 16, gen)
+    pool = P.Pool("bf16", pages, 16, heads, dim, "rows", gen)
+    q = torch.randn(sum(n) + 5, heads * group, dim, generator=gen).to(torch.bfloat16)
+    say(f"[gpu] {batch} sequences, {sum(n)} tokens")
+    if sum(n):
+        _tree(q, pool, table, lens, n, 16, max_len=max(lens))
+        _tree(q, pool, table, lens, n, 16, [w for t in n for w in _random_masks(gen, t, "tree")], max_len=max(lens))
+    else:
+        out = torch.full_like(q, 7.0, device="cuda")
+        L.tc_paged_tree_attention(q.cuda(), pool.on_gpu(), table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                  torch.zeros(batch + 1, dtype=torch.int32, device="cuda"), out=out)
+        assert bool((out == 7.0).all())
+
+
+def test_eight_times_the_sequences_take_eight_times_as_long():
+    """... and not the square of it (64 times): every workgroup finds its sequence among them in a few steps."""
+    took = []
+    for batch in (4096, 32768):
+        q = torch.randn(batch, 8, 64, device="cuda").to(torch.bfloat16)
+        starts = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+        out = torch.zeros_like(q)
+        call = lambda: L.tc_prompt_attention(q, q, q, starts, out=out)
+        call()
+        torch.cuda.synchronize()
+        best = 1e9
+        for _ in range(5):
+            t = time.perf_counter()
+            call()
+            torch.cuda.synchronize()
+            best = min(best, time.perf_counter() - t)
+        took.append(best)
+        assert torch.equal(out, q)  # a token alone sees itself
+    say(f"[gpu] {took[0] * 1e3:.2f} and {took[1] * 1e3:.2f} ms")
+    assert took[1] < 24 * took[0]

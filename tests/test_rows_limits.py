@@ -11,16 +11,26 @@ from test_rows_refusals import _prompt, _tree
 AT = 1 << 40
 
 
+def _sequences(workgroups, tile):
+    """So many one-token sequences make fewer workgroups, one more does not: a workgroup each, and one for each tile of tokens."""
+    n = workgroups * tile // (tile + 1) - 2
+    while n + 1 + (n + 1) // tile < workgroups:
+        n += 1
+    return n
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a call that passes the checks would be launched on made-up addresses")
-@pytest.mark.parametrize("dim, lanes", [(64, 256), (128, 256), (144, 512), (256, 512)])
-def test_attention_is_refused_only_past_its_own_grid(dim, lanes):
-    """Sequences of one token take a workgroup each, of eight waves for heads above 128 elements: calls of just under 2^32
-    lanes go on to the launch (which finds no GPU here), calls of 2^32 are refused."""
-    for tokens, want in ((2 ** 32 // lanes - 1, L.TC_E_HIP), (2 ** 32 // lanes, L.TC_E_RANGE)):
+@pytest.mark.parametrize("dim, lanes, prompt_tile, tree_tile", [(64, 256, 128, 64), (128, 256, 128, 64), (144, 512, 128, 128), (256, 512, 128, 128)])
+def test_attention_is_refused_only_past_its_own_grid(dim, lanes, prompt_tile, tree_tile):
+    """Workgroups have eight waves for heads above 128 elements: calls of just under 2^32 lanes go on to the launch (which
+    finds no GPU here), calls of 2^32 are refused."""
+    most = _sequences(2 ** 32 // lanes, prompt_tile)
+    for tokens, want in ((most, L.TC_E_HIP), (most + 1, L.TC_E_RANGE)):
         rc = _prompt(q_shape=(tokens, 1, dim), k_shape=(tokens, 1, dim), q=AT, k=2 * AT, v=3 * AT, out=4 * AT, starts=5 * AT, batch=tokens)
-        assert rc == want, ("prompt", tokens, rc, L.tc_last_error())
-        cache = _cache(shape=(PAGES, PAGE, 1, dim), k=6 * AT, v=7 * AT)
-        for dtype in (L.TC_BF16, L.TC_F16):
-            cache.dtype = dtype
+        assert rc == want, (tokens, rc, L.tc_last_error())
+    most = _sequences(2 ** 32 // lanes, tree_tile)
+    for dtype in (L.TC_BF16, L.TC_F16):
+        cache = _cache(dtype, shape=(PAGES, PAGE, 1, dim), k=6 * AT, v=7 * AT)
+        for tokens, want in ((most, L.TC_E_HIP), (most + 1, L.TC_E_RANGE)):
             rc = _tree(cache, dtype=dtype, q_shape=(tokens, 1, dim), q=AT, out=4 * AT, starts=5 * AT, lens=8 * AT, table=(tokens, 1), max_len=64)
-            assert rc == want, ("tree", tokens, rc, L.tc_last_error())
+            assert rc == want, (tokens, rc, L.tc_last_error())
