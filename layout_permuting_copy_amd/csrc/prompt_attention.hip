@@ -6,6 +6,7 @@ namespace dev {
 
 template <bool BF16, int DP>
 void prompt_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
+  if (shape.many) return attend_rows<BF16, 0, DP, (DP > 128 ? 4 : 2), (DP > 128 ? 8 : 4), 1, true>(a, s);
   if constexpr (DP > 64)
     if (shape.tile_rows == 256) return attend_rows<BF16, 0, DP, 8, 8, 1>(a, s);
   if constexpr (DP > 128) return attend_rows<BF16, 0, DP, 4, 8, 1>(a, s);
@@ -26,7 +27,7 @@ void prompt_by_dim(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
 
 int launch_prompt_attention(const RowsArgs& a, const RowsShape& shape, int dtype, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (!launchable(a.workgroups, rows_threads(a.head_dim, shape.tile_rows))) return TC_E_RANGE;
+  if (!launchable(a.workgroups, rows_threads(false, a.head_dim, shape.tile_rows, shape.many))) return TC_E_RANGE;
   if (dtype == TC_BF16)
     dev::prompt_by_dim<true>(a, shape, s);
   else

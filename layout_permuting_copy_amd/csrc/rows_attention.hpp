@@ -222,9 +222,9 @@ struct RowsWalk {
     }
     most = hi;
   }
-  // Whole tiles of many sequences (kRowsSummed): those of sequence b are numbered from (its first row over all sequences) / BM
-  // + b on.  Up to the next sequence's that leaves room for all of them, at most one number more, and the numbers ascend with
-  // b: the 64 lanes look for x's sequence in log64 of their count steps.
+  // Finds sequence and place of tile x of many sequences' (kRowsSummed): those of sequence b are numbered from (its first row
+  // over all sequences) / BM + b on.  Up to the next sequence's that leaves room for all of them, at most one number more, and
+  // the numbers ascend with b: the 64 lanes look for x's sequence in log64 of their count steps.
   static __device__ __forceinline__ uint32_t place(const RowsArgs& a, int b) {
     return uint32_t(within(a.starts[b], 0, a.tokens) * a.group) / BM + uint32_t(b);
   }
@@ -237,6 +237,7 @@ struct RowsWalk {
       lo += skip;
       span = step < span - skip ? step : span - skip;
     }
+    lo = __builtin_amdgcn_readfirstlane(lo);
     const RowsSeq q = rows_seq<PAGED>(a, lo);
     s->t0 = __builtin_amdgcn_readfirstlane(q.t0), s->n = __builtin_amdgcn_readfirstlane(q.n);
     s->k0 = __builtin_amdgcn_readfirstlane(q.k0), s->m = __builtin_amdgcn_readfirstlane(q.m);
@@ -248,7 +249,6 @@ struct RowsWalk {
   // number of the sequence's first item of parts.
   template <bool REVERSED, bool ITEMS>
   __device__ __forceinline__ bool find(const RowsArgs& a, uint32_t x, int* b, uint32_t* at, uint32_t* first, RowsSeq* s) const {
-    if (a.batch > kRowsSummed && !a.slots) return find_among_many(a, REVERSED ? uint32_t(a.tiles) - 1 - x : x, b, at, s);
     const int lane = threadIdx.x & 63;
     uint32_t sum = 0, all = 0;
     for (int k = 0; k < per && lane * per + k < a.batch; ++k) {
@@ -365,7 +365,9 @@ struct Rows {
 // which leaves 7 % of waits; two waves a SIMD that take turns by barriers, one multiplying while the other softens, came to
 // 2371 us, as a wave alone does not hide the reads of its operands); trees of few tokens by what a CU has in flight (32 trees of 8
 // tokens over 4096 rows: 115 us, 4.7 TB/s); 8-bit caches by the conversions (16 trees of 12 tokens over 8192 rows: 127 us).
-template <bool BF16, int SRC, int DP, int WQ, int WAVES_, int PARTS>
+// MANY: of many sequences (RowsWalk::find_among_many), a kernel of its own, as the others' scalar registers do not suffice for
+// both ways (32 trees of 26 tokens 62 -> 67 us).
+template <bool BF16, int SRC, int DP, int WQ, int WAVES_, int PARTS, bool MANY>
 __global__ __launch_bounds__(64 * WAVES_, (Rows<BF16, SRC, DP, WQ, WAVES_, PARTS>::RESIDENT * WAVES_ / 4))
 void rows_attention_kernel(RowsArgs a) {
   typedef Rows<BF16, SRC, DP, WQ, WAVES_, PARTS> C;
@@ -382,13 +384,17 @@ void rows_attention_kernel(RowsArgs a) {
   const int h = int(blockIdx.x - x * a.heads_div.d);
 
   RowsWalk<PAGED, BM, KT> walk;
-  walk.template init<true>(a);
-  if (a.slots && blockIdx.x == 0 && tid == 0) *a.part_units = walk.most;
   int b;
   uint32_t at, first;
   RowsSeq seq;
-  if (!walk.template find<!PAGED, true>(a, x, &b, &at, &first, &seq)) return;
-  const int tiles = int(walk.tiles(a, seq)), parts = __builtin_amdgcn_readfirstlane(int(walk.parts(a, seq)));
+  if constexpr (MANY) {
+    if (!walk.find_among_many(a, PAGED ? x : uint32_t(a.tiles) - 1 - x, &b, &at, &seq)) return;
+  } else {
+    walk.template init<true>(a);
+    if (a.slots && blockIdx.x == 0 && tid == 0) *a.part_units = walk.most;
+    if (!walk.template find<!PAGED, true>(a, x, &b, &at, &first, &seq)) return;
+  }
+  const int tiles = int(walk.tiles(a, seq)), parts = MANY ? 1 : __builtin_amdgcn_readfirstlane(int(walk.parts(a, seq)));
   const int part = parts > 1 ? int(at / uint32_t(tiles)) : 0, tile = int(at) - part * tiles;
   const int rows = seq.n * a.group, row0 = tile * BM;
   const int off = seq.m - seq.n;  // token i's own row
@@ -511,6 +517,8 @@ void rows_attention_kernel(RowsArgs a) {
     return (u + 1) * KT > clear || (u + 1) * KT > seq.m || missing != 0;
   };
 
+  // (hl, found anew where that saves its register)
+  const auto half = [&] { return MANY && DP > 192 ? fresh(int(threadIdx.x)) >> 5 & 1 : hl; };
   f32x16 o[NF];
   float m = -kInf, l = 0.0f;
 #pragma unroll
@@ -612,7 +620,7 @@ void rows_attention_kernel(RowsArgs a) {
         } else {
           w = low_bits(limit - key0 + 1);
         }
-        seen[n] = (w & ~gone) >> 4 * hl;
+        seen[n] = (w & ~gone) >> 4 * half();
       }
       // A weight of 0 does not help against infinite or NaN values of rows that are not seen.  Where the tile has any,
       // each query's output first takes the infinities and NaN of the rows that it does see, as products of numbers that
@@ -713,7 +721,7 @@ void rows_attention_kernel(RowsArgs a) {
         for (int n = 0; n < NJ; ++n)
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(&scales[buf][0][(wg * NSUB + n0 + n) * 32 + 2 * i + 4 * hl]);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&scales[buf][0][(wg * NSUB + n0 + n) * 32 + 2 * i + 4 * half()]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[n][i + j] *= x[j];
           }
@@ -770,7 +778,7 @@ void rows_attention_kernel(RowsArgs a) {
         for (int n = 0; n < NJ; ++n) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(&scales[buf][1][(wg * NSUB + n0 + n) * 32 + 2 * i + 4 * hl]);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&scales[buf][1][(wg * NSUB + n0 + n) * 32 + 2 * i + 4 * half()]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[n][i + j] = weight(n, i + j) * x[j];
           }
@@ -858,13 +866,18 @@ void rows_attention_kernel(RowsArgs a) {
       const float theirs = __builtin_amdgcn_exp2f((meet_ml[at][0][end_lane] - ref) * c);
       l += meet_ml[at][1][end_lane] * theirs;
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
+      for (int f = 0; f < NF; ++f) {
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const f32x4 x = *reinterpret_cast<const f32x4*>(meet + ((at * NF + f) * 4 + i / 4) * 256 + end_lane * 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[f][i + j] += x[j] * theirs;
+          for (int j = 0; j < 4; ++j) {
+            float y = o[f][i + j] + x[j] * theirs;
+            if constexpr (MANY && DP > 192) asm volatile("" : "+v"(y));  // (now, not behind the stores before it: x's registers)
+            o[f][i + j] = y;
+          }
         }
+      }
     }
     m = top;
   }

@@ -54,6 +54,8 @@ RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int6
     c.workgroups = (c.workgroups + fill - 1) / fill * fill;
     c.bytes = kRowsWorkspaceHead + c.workgroups * c.tile_rows * (head_dim + 2) * 4;
   } else if (batch > kRowsSummed) {
+    c.many = true;
+    c.tile_rows = least_tile(head_dim);
     c.tiles = rows / c.tile_rows + batch;  // as RowsWalk::place numbers them
     c.workgroups = c.tiles * heads;
   }

@@ -12,7 +12,7 @@ void tree_attention_e4m3_bf16(const RowsArgs& a, const RowsShape& shape, hipStre
 
 int launch_tree_attention(const RowsArgs& a, const RowsShape& shape, int dtype, int cache_dtype, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (!launchable(a.workgroups, rows_threads(a.head_dim, shape.tile_rows))) return TC_E_RANGE;
+  if (!launchable(a.workgroups, rows_threads(cache_dtype == TC_E4M3, a.head_dim, shape.tile_rows, shape.many))) return TC_E_RANGE;
   const bool bf16 = dtype == TC_BF16;
   if (cache_dtype == TC_E4M3)
     bf16 ? tree_attention_e4m3_bf16(a, shape, s) : tree_attention_e4m3_f16(a, shape, s);

@@ -12,6 +12,8 @@ namespace dev {
 template <bool BF16, int SRC, int DP, int PARTS>
 void tree_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
   constexpr int LARGE = SRC == 2 && !BF16 ? 2 : 1;
+  // (of many sequences' wide 8-bit rows: eight waves would need scratch memory there)
+  if (shape.many) return attend_rows<BF16, SRC, DP, (DP > 128 ? 4 : 2), (DP > 128 && SRC != 2 ? 8 : 4), (DP > 128 ? LARGE : PARTS), true>(a, s);
   if constexpr (DP > 64 && !(SRC == 2 && DP > 128))
     if (shape.tile_rows == 256) return attend_rows<BF16, SRC, DP, 8, 8, LARGE>(a, s);
   if constexpr (DP > 128) return attend_rows<BF16, SRC, DP, 4, 8, LARGE>(a, s);

@@ -191,6 +191,27 @@ def test_trees_of_many_sequences(pattern, batch, heads, group, dim):
         assert bool((out == 7.0).all())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "bf16-e4m3", "fp16-e4m3"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_many_sequences_in_every_width(kind, dim):
+    """1600 sequences, a few of which have tokens: more than a tile of them, one, none of their rows seen."""
+    gen = torch.Generator().manual_seed(dim)
+    kinds = kind.split("-")
+    n = [0] * 1600
+    n[0], n[3], n[700], n[701], n[1598], n[1599] = 3, 140, 1, 64, 70, 2
+    lens = [3 * x // 2 + (x > 0) for x in n]
+    lens[701] = 0
+    table, pages = P.table_for(lens, 16, gen)
+    pool = P.Pool(kinds[-1], pages, 16, 1, dim, "rows", gen)
+    q = torch.randn(sum(n) + 3, 2, dim, generator=gen).to(P.DT[kinds[0]])
+    say(f"[gpu] {kind} heads of {dim}")
+    _tree(q, pool, table, lens, n, 16, max_len=max(lens))
+    if len(kinds) == 1:
+        k, v = (torch.randn(sum(n) + 3, 1, dim, generator=gen).to(q.dtype) for _ in range(2))
+        for causal in (True, False):
+            _prompt(q, k, v, n, causal=causal)
+
+
 def test_eight_times_the_sequences_take_eight_times_as_long():
     """... and not the square of it (64 times): every workgroup finds its sequence among them in a few steps."""
     took = []

@@ -31,7 +31,7 @@ def _built():
         names = " ".join(json.load(f))
     found = set()
     for bf16 in "01":
-        one = {(int(s), int(d), 32 * int(w)) for s, d, w in re.findall(rf"rows_attention_kernelILb{bf16}ELi(\d)ELi(\d+)ELi(\d)E", names)}
+        one = {(int(s), int(d), 32 * int(w)) for s, d, w in re.findall(rf"rows_attention_kernelILb{bf16}ELi(\d)ELi(\d+)ELi(\d)ELi\dELi\dELb0E", names)}
         assert one and (not found or one == found)
         found = one
     return found
