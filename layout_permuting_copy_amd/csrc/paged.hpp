@@ -159,18 +159,12 @@ int64_t paged_logit_row(int64_t max_len);
 // card filled by parts of tiles (slots, least as in RowsArgs) where tiles are few.
 struct RowsShape {
   int64_t tile_rows, unit_rows, tiles, slots, least, workgroups, bytes;
-  bool many;  // tiles are numbered as those of many sequences (kRowsSummed)
+  bool many;  // tiles are numbered as those of many sequences
 };
 // Lanes of a workgroup: eight waves for wide heads and the largest tiles, else four, as for many sequences' 8-bit rows.
 constexpr int64_t rows_threads(bool codes, int64_t head_dim, int64_t tile_rows, bool many) {
   return (head_dim > 128 && !(many && codes)) || tile_rows == 256 ? 512 : 256;
 }
-// Up to so many sequences a workgroup adds up the tiles before its own, each wave all of them; whole tiles of more, the least ones
-// then, are numbered so that few steps find one, with a number for nobody a sequence where tiles are full.  (Trees of 16 tokens, 8
-// heads a group, 1 key head, over 256 rows: 512 sequences added up 32 us, numbered 43; 1537 115 and 114; 2048 217 and 160.
-// Prompts of 32 tokens, 4 heads a group, 8 key heads: 512 123 and 151, 1537 563 and 355, 4096 4465 and 948.  Prompts of one token,
-// 8 heads: 32768 142 ms and 2.7.)
-constexpr int64_t kRowsSummed = 1536;
 constexpr int64_t kRowsWorkspaceHead = 256;  // bytes: a number, and the parts on lines of their own
 RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int64_t heads, int64_t group, int64_t head_dim, int64_t max_len);
 // Bytes that suffice for the parts of tiles at these sizes and at any smaller batch, tokens and max_len.

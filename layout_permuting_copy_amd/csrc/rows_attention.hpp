@@ -222,7 +222,7 @@ struct RowsWalk {
     }
     most = hi;
   }
-  // Finds sequence and place of tile x of many sequences' (kRowsSummed): those of sequence b are numbered from (its first row
+  // Finds sequence and place of tile x of many sequences': those of sequence b are numbered from (its first row
   // over all sequences) / BM + b on.  Up to the next sequence's that leaves room for all of them, at most one number more, and
   // the numbers ascend with b: the 64 lanes look for x's sequence in log64 of their count steps.
   static __device__ __forceinline__ uint32_t place(const RowsArgs& a, int b) {
@@ -366,7 +366,7 @@ struct Rows {
 // 2371 us, as a wave alone does not hide the reads of its operands); trees of few tokens by what a CU has in flight (32 trees of 8
 // tokens over 4096 rows: 115 us, 4.7 TB/s); 8-bit caches by the conversions (16 trees of 12 tokens over 8192 rows: 127 us).
 // MANY: of many sequences (RowsWalk::find_among_many), a kernel of its own, as the others' scalar registers do not suffice for
-// both ways (32 trees of 26 tokens 62 -> 67 us).
+// both ways (32 trees of 26 tokens 62 us, in such a kernel 67).
 template <bool BF16, int SRC, int DP, int WQ, int WAVES_, int PARTS, bool MANY>
 __global__ __launch_bounds__(64 * WAVES_, (Rows<BF16, SRC, DP, WQ, WAVES_, PARTS>::RESIDENT * WAVES_ / 4))
 void rows_attention_kernel(RowsArgs a) {

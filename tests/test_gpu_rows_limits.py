@@ -145,7 +145,7 @@ def _counts(pattern, batch):
     return [few[pattern](i) for i in range(batch)]
 
 
-MANY = [(p, b) for p in ("ones", "sparse", "ragged", "one long", "last", "first", "none") for b in (65, 1537)] + [("ragged", 1536), ("sparse", 5000)]
+MANY = [(p, b) for p in ("ones", "sparse", "ragged", "one long", "last", "first", "none") for b in (65, 2500)] + [("ragged", 2048), ("sparse", 5000)]
 
 
 @pytest.mark.parametrize("pattern, batch", MANY)
@@ -171,7 +171,7 @@ def test_prompts_of_many_sequences(pattern, batch, heads, group, dim, lead):
     assert bool((out[rest.cuda()] == 7.0).all()) and bool((lse[rest.cuda()] == 7.0).all())
 
 
-@pytest.mark.parametrize("pattern, batch", [(p, b) for p, b in MANY if b < 2000])
+@pytest.mark.parametrize("pattern, batch", [(p, b) for p, b in MANY if b < 3000])
 @pytest.mark.parametrize("heads, group, dim", [(1, 4, 64), (1, 1, 192)])
 def test_trees_of_many_sequences(pattern, batch, heads, group, dim):
     gen = torch.Generator().manual_seed(batch)
@@ -194,11 +194,11 @@ def test_trees_of_many_sequences(pattern, batch, heads, group, dim):
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "bf16-e4m3", "fp16-e4m3"])
 @pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
 def test_many_sequences_in_every_width(kind, dim):
-    """1600 sequences, a few of which have tokens: more than a tile of them, one, none of their rows seen."""
+    """2600 sequences, a few of which have tokens: more than a tile of them, one, none of their rows seen."""
     gen = torch.Generator().manual_seed(dim)
     kinds = kind.split("-")
-    n = [0] * 1600
-    n[0], n[3], n[700], n[701], n[1598], n[1599] = 3, 140, 1, 64, 70, 2
+    n = [0] * 2600
+    n[0], n[3], n[700], n[701], n[2598], n[2599] = 3, 140, 1, 64, 70, 2
     lens = [3 * x // 2 + (x > 0) for x in n]
     lens[701] = 0
     table, pages = P.table_for(lens, 16, gen)
