@@ -20,7 +20,7 @@ RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int6
   const int64_t rows = tokens * group;
   if (paged) {
     // A cache's rows are read once a tile: tiles that hold a sequence's query rows, of 128 from half that many on (32 trees of
-    // 26 tokens, 4 heads a group: 69 us, in tiles of 64 rows 84).  Half empty ones cost more than the rows read twice save
+    // 26 tokens, 4 heads a group: 69 us, in tiles of 64 rows, whose bf16 weights keep more bits, 84).  Half empty ones cost more than the rows read twice save
     // from there down (16 trees of 64 rows over 8-bit caches: 112 us, in tiles of 128 rows 160).
     c.tile_rows = least_tile(head_dim);
     while (c.tile_rows < 128 && c.tile_rows * batch < 2 * rows) c.tile_rows *= 2;
@@ -37,7 +37,9 @@ RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int6
     if (tiles_of(rows, batch, 128) * heads >= 4 * kCus) c.tile_rows = 128;
     if (head_dim > 64 && tiles_of(rows, batch, 256) * heads >= 2 * kCus && rows >= 2048 * batch) c.tile_rows = 256;
   }
-  // Tiles that leave half of the card idle are split over their keys: a cache's always, unless they are short, a prompt's where
+  // Tiles that leave half of the card idle are split over their keys: a cache's always, unless they are short (trees of 8 tokens, 32
+  // heads over 8, whole and split, us: one over 256 rows 13.4 and 16.2, over 512 19.6 and 16.5, over 1024 31.8 and 17.6; 8 over 256
+  // 13.6 and 17.3, over 512 19.9 and 18.7, over 1024 33.0 and 22.7; 32 over 512 22.0 and 28.2, over 1024 34.6 and 37.4), a prompt's where
   // its keys (`max_len` is their mean) are long enough for the joining to pay (64 tokens of 32 heads over 8, 8064 keys: 145 us,
   // split 33; 512 of 8 over 1, 4608 keys: 85 and 35; 1024 causal tokens of 8 over 8: 24 and 27).  Prompts whose tiles come to
   // more are faster whole (2048 tokens of 16 heads of 256 over 4: 86 us, split 92).
@@ -53,12 +55,13 @@ RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int6
     // all parts fit the least multiple of `fill` that the tiles do
     c.workgroups = (c.workgroups + fill - 1) / fill * fill;
     c.bytes = kRowsWorkspaceHead + c.workgroups * c.tile_rows * (head_dim + 2) * 4;
-  } else if (batch > std::max<int64_t>(2048, 8 * std::min<int64_t>(max_len, 1536))) {
+  } else if (batch > 12288 || (c.tile_rows < 256 && batch > std::max<int64_t>(1024, 8 * max_len))) {
     // Adding up the tiles before its own costs a workgroup time in proportion to the sequences; finding them by numbers, a few
-    // steps, with a number for nobody a sequence where tiles are full, and the least tiles, which read long caches more often.
-    // (Added up and numbered, us: 2049 prompts of 8 tokens, 8 heads, 657 and 182, of 340 tokens, 32 heads over 8, 9590 and 7273;
-    // chunks of 64 tokens, 8 heads over 1: 2049 over 100 rows 470 and 337, over 340 614 and 672, 6145 over 1000 4303 and 3874, over
-    // 2000 6079 and 7173; 32768 prompts of one token, 8 heads, 142000 and 2700.)
+    // steps, with a number for nobody a sequence where tiles are full, and the least tiles, which read long keys more often.
+    // (Added up and numbered, us: 2049 prompts of 8 tokens, 8 heads, 657 and 182, 1025 of 32, 32 heads over 8, 320 and 239; 1025
+    // trees of 8 tokens, 8 heads over 1, over 128 rows 46 and 51, 1400 64 and 63; with sequences that fill tiles of 256 rows, chunks
+    // of 64 tokens, 8 heads over 1: 2049 over 340 rows 614 and 672, 6145 over 2000 6079 and 7173; 32768 prompts of one token, 8
+    // heads, 142000 and 2700.)
     c.many = true;
     c.tile_rows = least_tile(head_dim);
     c.tiles = rows / c.tile_rows + batch;  // as RowsWalk::place numbers them

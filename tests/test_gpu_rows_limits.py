@@ -145,7 +145,7 @@ def _counts(pattern, batch):
     return [few[pattern](i) for i in range(batch)]
 
 
-MANY = [(p, b) for p in ("ones", "sparse", "ragged", "one long", "last", "first", "none") for b in (65, 2500)] + [("ragged", 2048), ("sparse", 5000)]
+MANY = [(p, b) for p in ("ones", "sparse", "ragged", "one long", "last", "first", "none") for b in (65, 2500)] + [("ragged", 1000), ("sparse", 5000)]
 
 
 @pytest.mark.parametrize("pattern, batch", MANY)
