@@ -361,7 +361,7 @@ struct Rows {
 // there without bank conflicts, values transposed on the way out.  All waves share the unit; where there are fewer tiles of
 // 32 query rows than waves, groups of waves share out its rows and meet at the end.
 // Bound: with prompts and chunks the matrix products and the softmax's vector instructions in turn (16384 causal tokens, 32
-// heads of 128 over 8: 2065 us, 1065 TFLOP/s; the matrix units are busy 51 % of the time, vector instructions issue in 42 %,
+// heads of 128 over 8: 2080 us, 1057 TFLOP/s; the matrix units are busy 51 % of the time, vector instructions issue in 42 %,
 // which leaves 7 % of waits; two waves a SIMD that take turns by barriers, one multiplying while the other softens, came to
 // 2371 us, as a wave alone does not hide the reads of its operands); trees of few tokens by what a CU has in flight (32 trees of 8
 // tokens over 4096 rows: 115 us, 4.7 TB/s); 8-bit caches by the conversions (16 trees of 12 tokens over 8192 rows: 127 us).
@@ -451,7 +451,7 @@ void rows_attention_kernel(RowsArgs a) {
     return Place{uint32_t(e) < uint32_t(a.pool.pages) ? e : 0,
                  int64_t(uint32_t(key) - udiv(uint32_t(key), a.pool.div) * a.pool.div.d)};
   };
-  // Requests unit u, rows past the end as the last one.  Rows go from memory into LDS as they are, a wave's lanes side by
+  // Requests unit u; of rows past the end: zeros (packed: outside the range, which counts the scalar offset) or the last one.  Rows go from memory into LDS as they are, a wave's lanes side by
   // side: what is exchanged is which chunk a lane loads.
   // (the rows that a wave loads at once lie on one page: its address is the wave's)
   const bool page_wise = PAGED && a.pool.page_size % C::RPW == 0 && a.pool.kr < 1 << 26 && a.pool.vr < 1 << 26;

@@ -7,8 +7,9 @@ namespace tc {
 namespace dev {
 
 // 8-bit rows' weights are bf16 values, as their scales may pass fp16's range: for fp16 queries the sum of two in every tile (one
-// holds 8 bits, fewer than out; 16 trees of 12 tokens over 8192 rows 153 us, with one 133), else in tiles of 64 rows, whose
-// matrix units wait for memory anyway.
+// holds 8 bits, fewer than out; 16 trees of 12 tokens over 8192 rows 153 us, with one 133).  bf16 queries' are the sum of two in
+// tiles of 64 rows of heads of up to 128 elements, whose matrix units wait for memory anyway, else one (32 trees of 26 tokens:
+// rms error against 64 bits 0.0022, in tiles of 64 rows 0.0017, which is out's own rounding; over 8-bit rows 0.0023 and 0.0017).
 template <bool BF16, int SRC, int DP, int PARTS>
 void tree_by_tile(const RowsArgs& a, const RowsShape& shape, hipStream_t s) {
   constexpr int LARGE = SRC == 2 && !BF16 ? 2 : 1;
