@@ -8,7 +8,7 @@ import layout_permuting_copy_amd as L
 import paged_ref as P
 import rows_ref as R
 from gpu_util import say
-from test_gpu_rows import LARGE, TREES, _i32, _prompt_ref, _qkv, _tree_ref
+from test_gpu_rows import LARGE, TREES, _i32, _prompt, _prompt_ref, _qkv, _random_masks, _tree, _tree_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,19 @@ def test_fp16_trees_lose_only_what_subnormal_weights_do(shape):
         ref = R.sequence(q[a:a + t], k, v, R.before(t, m))
         R.close(out[a:a + t], ref[0], ref[2], f"out of sequence {b}", torch.float16)
         a += t
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("group", [33, 65, 300])
+def test_groups_of_more_heads_than_a_tile_has_rows(kind, group):
+    """One key head under many query heads: a token's rows begin anywhere in a tile and end in another."""
+    gen = torch.Generator().manual_seed(group)
+    dt, dim, lens, n = P.DT[kind] if kind != "e4m3" else torch.bfloat16, 64, [90, 0, 700], [3, 0, 5]
+    if kind != "e4m3":
+        _prompt(*_qkv(gen, dt, 12, 12, 1, group, dim), [4, 0, 1, 6])
+    table, pages = P.table_for(lens, 16, gen)
+    pool = P.Pool(kind, pages, 16, 1, dim, "rows", gen)
+    q = torch.randn(sum(n) + 1, group, dim, generator=gen).to(dt)
+    say(f"[gpu] {group} heads a group")
+    _tree(q, pool, table, lens, n, 16)
+    _tree(q, pool, table, lens, n, 16, [w for t in n for w in _random_masks(gen, t, "any")])
