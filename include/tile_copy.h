@@ -486,7 +486,8 @@ int tc_paged_resize(int32_t* block_table, const tc_layout* table_layout, const i
  * relative to a reference that lags the maximum by 2^8 at most: as one value (8 bits of bf16, 11 of fp16), or as the sum of two,
  * for TC_F16 over TC_E4M3 always, for TC_BF16 with head_dim up to 128 where the call has at most 32 query rows (tokens times
  * q_heads / heads) a sequence on average, or thousands of sequences.  So what a sequence's weights keep depends on the others
- * of its call.  Rows that are not seen, past n or on no page are never used, whatever they hold; an infinite or NaN value
+ * of its call.  Over TC_E4M3 a weight is rounded with its v_scale in it, below 2^-126 to multiples of 2^-133, and an element of
+ * out may be infinite or NaN from sums of exp(x - max x) |v|, or a v_scale, of 2^119 on.  Rows that are not seen, past n or on no page are never used, whatever they hold; an infinite or NaN value
  * in a row that is seen makes its element of out infinite or NaN.  Equal calls give equal bits; how rows are dealt out, and with it
  * the last bits of sums, depends on the whole batch and max_len.  Tokens from starts[batch] on are padding: their rows of out and lse
  * are left as they are.  lse (tokens, q_heads), fp32, may be NULL.

@@ -59,13 +59,45 @@ def test_tree_values_near_the_end_of_the_range(kind, dim, tokens, rows):
         P.bits(pool.k)[at, row] = codes(k.float().sign())
         pool.ks[at, row] = k.float().amax(-1)
         P.bits(pool.v)[at, row] = codes(v / v.abs().amax(-1, keepdim=True))
-        pool.vs[at, row] = v.abs().amax(-1)
+        pool.vs[at, row] = v.abs().amax(-1) / 2048  # 2^119 is promised there
     else:
         pool.k[at, row], pool.v[at, row] = k, v.to(torch.bfloat16)
     say(f"[gpu] {tokens} tokens over {rows} rows of {dim}")
     for words in (None, _random_masks(gen, tokens, "tree")):
         out, _, ref = _tree(q, pool, table, [rows], [tokens], 16, words, scale=1.0, max_len=rows)
-        assert bool(out.isfinite().all()) and float(ref[0].abs().max()) > 1e36 / rows
+        assert bool(out.isfinite().all()) and float(ref[0].abs().max()) > (1e36 if kind == "bf16" else 1e33) / rows
+
+
+@pytest.mark.parametrize("exponent", [-126, -118, -110, 0, 118])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim, tokens, rows", [(64, 5, 300), (128, 70, 300), (256, 5, 4000)])
+def test_tree_scales_of_either_end(exponent, dtype, dim, tokens, rows):
+    """Scales from the least normal number to near the greatest that are promised to work, under a maximum that grows slower
+    than what the reference follows, with codes of one sign: nothing overflows, and no bits are lost but those that numbers below
+    2^-126 have not: of weights times scales (half of 2^-133 each, times a code of 448, the sum of weights being at least 1) and
+    of out."""
+    gen = torch.Generator().manual_seed(dim)
+    table, pages = P.table_for([rows], 16, gen)
+    pool = P.Pool("e4m3", pages, 16, 1, dim, "rows", gen)
+    q, k, _ = _rising(rows, 1, dim, tokens, 2, rows // 15, gen)
+    q = q.to(P.DT[dtype])
+    at, row = table[0][torch.arange(rows) // 16].long(), torch.arange(rows) % 16
+    P.bits(pool.k)[at, row] = P.bits(k.float().sign().to(torch.float8_e4m3fn))
+    pool.ks[at, row] = k.float().amax(-1)
+    most = 14.0 / rows if exponent > 100 else 448.0  # sums of all rows stay below 2^119
+    P.bits(pool.v)[at, row] = P.bits((torch.rand(rows, 1, dim, generator=gen) * most / 2 + most / 2).to(torch.float8_e4m3fn))
+    pool.vs.fill_(2.0 ** exponent)
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")
+    out = L.tc_paged_tree_attention(q.cuda(), pool.on_gpu(), table.cuda(), i32([rows]), i32([0, tokens]), scale=1.0, max_len=rows)
+    say(f"[gpu] scales of 2^{exponent}")
+    if dtype == "fp16" and exponent > 0:
+        assert bool((out == torch.inf).all())  # past fp16's own range
+        return
+    kr, vr = (pool.rows(x, table[0], rows, 16)[0] for x in "kv")
+    ref = R.sequence(q, kr, vr, R.before(tokens, rows), 1.0, 2.0 ** -8)
+    lost = 2.0 ** -134 * 448 * rows + (2.0 ** -134 if dtype == "bf16" else 2.0 ** -25)
+    assert bool(out.isfinite().all())
+    R.close(out, ref[0], ref[2] + lost, "out", q.dtype)
 
 
 def _far(kind, x, rows, tokens, dim, gen):
