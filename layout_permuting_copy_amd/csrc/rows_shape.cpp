@@ -20,8 +20,8 @@ RowsShape rows_shape(bool paged, bool codes, int64_t batch, int64_t tokens, int6
   const int64_t rows = tokens * group;
   if (paged) {
     // A cache's rows are read once a tile: tiles that hold a sequence's query rows, of 128 from half that many on (32 trees of
-    // 26 tokens, 4 heads a group: 69 us, in tiles of 64 rows, whose bf16 weights keep more bits, 84).  Half empty ones cost more than the rows read twice save
-    // from there down (16 trees of 64 rows over 8-bit caches: 112 us, in tiles of 128 rows 160).
+    // 26 tokens, 4 heads a group: 69 us, in tiles of 64 rows, whose bf16 weights keep more bits, 84).  Half empty ones cost more
+    // than the rows read twice save from there down (16 trees of 64 rows over 8-bit caches: 112 us, in tiles of 128 rows 160).
     c.tile_rows = least_tile(head_dim);
     while (c.tile_rows < 128 && c.tile_rows * batch < 2 * rows) c.tile_rows *= 2;
     // ... and of 256, by eight waves, once they are full (trees of 64 tokens, 8 heads a group, over 65536 rows: 356 -> 312 us;
